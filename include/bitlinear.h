@@ -64,7 +64,8 @@ typedef enum {
     BL_ERR_CUDA = 5,      /* a CUDA runtime call or kernel launch failed */
     BL_ERR_TIMEOUT = 6,   /* a bounded device-side wait gave up (see bl_check_device_error) */
     BL_ERR_WORKSPACE = 7, /* workspace NULL or smaller than the *_workspace_bytes query */
-    BL_ERR_DEVICE = 8     /* the current device is not a compute capability 10.x GPU */
+    BL_ERR_DEVICE = 8,    /* the current device is not a compute capability 10.x GPU */
+    BL_ERR_INDEX = 9      /* an index on the device lies outside its array (see bl_check_device_error) */
 } bl_status;
 
 typedef enum {
@@ -78,9 +79,10 @@ const char *bl_status_string(bl_status s);
 /* Library ABI version (major * 100 + minor). */
 int bl_version(void);
 
-/* Reads and clears the device error word set by bounded device-side waits.
- * Synchronizes `stream` first.  Returns BL_OK, BL_ERR_TIMEOUT or
- * BL_ERR_CUDA. */
+/* Reads and clears the device error word set by bounded device-side waits
+ * and by the kernels' checks of indexes that live on the device
+ * (bitlinear_attn.h).  Synchronizes `stream` first.  Returns BL_OK,
+ * BL_ERR_TIMEOUT, BL_ERR_INDEX or BL_ERR_CUDA. */
 bl_status bl_check_device_error(bl_stream_t stream);
 
 /* ------------------------------------------------------------------------ */

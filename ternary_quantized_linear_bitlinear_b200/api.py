@@ -1,4 +1,4 @@
-"""Python binding of libbitlinear.so (include/bitlinear.h).
+"""Python binding of libbitlinear.so (include/bitlinear.h, include/bitlinear_attn.h).
 
 Argument marshalling only: every function here checks that torch tensors are
 CUDA tensors on the current device, contiguous, of the right dtype and large
@@ -10,6 +10,7 @@ the library's kernels; if the library is missing, loading fails loudly.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -63,6 +64,12 @@ class DecodeProblem(ctypes.Structure):
                 ("s", _p), ("acc_out", _p), ("N", _i64), ("K", _i64)]
 
 
+class KvCache(ctypes.Structure):
+    """bl_kv_cache: the paged cache of one layer, as the kernels see it."""
+    _fields_ = [("k_pages", _p), ("v_pages", _p), ("tables", _p), ("lengths", _p), ("num_pages", _i64),
+                ("page_size", _i64), ("max_seqs", _i64), ("max_pages", _i64), ("dtype", _int)]
+
+
 _SIGS = {
     "bl_status_string": (ctypes.c_char_p, [_int]),
     "bl_version": (_int, []),
@@ -90,6 +97,21 @@ _SIGS = {
     "bl_linear_grouped_workspace_bytes": (_sz, [ctypes.POINTER(LinearProblem), _int, _i64, _i64]),
     "bl_linear_grouped": (_int, [ctypes.POINTER(LinearProblem), _int, _int, _p, _int, _i64, _i64, _p, _f32, _p, _sz,
                                  _p]),
+    "bl_rope_append": (_int, [_p, _p, _p, _int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _p, _i64, _int, _p, _i64, _p,
+                              _p, _i64, ctypes.POINTER(KvCache), _p, _p, _p, _int, _p]),
+    "bl_attn_decode_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "bl_attn_decode": (_int, [_p, _int, _i64, _i64, _i64, _i64, _i64, ctypes.POINTER(KvCache), _p, _i64, _i64, _f32, _p,
+                              _sz, _p, _p, _p]),
+    "bl_kv_extend": (_int, [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _p]),
+    "bl_kv_free": (_int, [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _i64, _p]),
+    "bl_kv_fork_workspace_bytes": (_sz, [_i64]),
+    "bl_kv_fork": (_int, [_p, _i64, _i64, _p, _p, _p, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _sz, _p, _p]),
+    "bl_kv_compact_workspace_bytes": (_sz, [_i64]),
+    "bl_kv_compact": (_int, [_p, _i64, _i64, _p, _p, _i64, _i64, _i64, _p, _sz, _p, _p]),
+    "bl_attn_forward": (_int, [_p, _p, _p, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _p, _p, _i64, _i64, _i64,
+                               _i64, _i64, _f32, _p, _p, _p]),
+    "bl_attn_backward_workspace_bytes": (_sz, [_i64] * 10),
+    "bl_attn_backward": (_int, [_p] * 6 + [_i64] * 9 + [_p, _p] + [_i64] * 5 + [_f32, _p, _sz, _p, _p, _p, _p]),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -556,6 +578,334 @@ def bl_linear_grouped(Ws, X, subln_gain=None, subln_eps: float = 1e-6, Ys=None, 
                                  subln_eps, workspace.data_ptr(), workspace.numel(), _stream(stream))
     _check(rc, "bl_linear_grouped")
     return Ys
+
+
+# -- attention and its cache (include/bitlinear_attn.h) ------------------------
+
+def _rows3(t, name: str, heads: int | None = None, D: int | None = None, dtype=None, rows: int | None = None):
+    """Rows of heads [T, H, D] on the current device whose heads are contiguous
+    (a row may be part of a wider one) -> row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D [T, heads, D], got shape {tuple(t.shape)}")
+    if not _is_cuda(t):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if _device_index(t) != _current_device():
+        raise ValueError(f"{name} lives on cuda:{_device_index(t)}, the current device is cuda:{_current_device()}")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    T, H, d = t.shape
+    for what, got, want in (("rows", T, rows), ("heads", H, heads), ("as head size", d, D)):
+        if want is not None and got != want:
+            raise ValueError(f"{name} has {got} {what}, expected {want}")
+    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    stride = t.stride(0) if T > 1 else H * d
+    if stride < H * d:
+        raise ValueError(f"{name}: rows overlap (stride {stride}, {H * d} elements each)")
+    return stride
+
+
+def _i32(t, name: str, numel: int):
+    _dev(t, name, torch.int32)
+    if t.numel() != numel:
+        raise ValueError(f"{name} holds {t.numel()} elements, expected {numel}")
+    return t
+
+
+def _tables2(tables, lengths, refs=None):
+    _dev(tables, "tables", torch.int32)
+    if tables.dim() != 2:
+        raise ValueError("tables must be 2-D [max_seqs, max_pages]")
+    if lengths is not None:
+        _i32(lengths, "lengths", tables.shape[0])
+    if refs is not None:
+        _dev(refs, "refs", torch.int32)
+        if refs.dim() != 1:
+            raise ValueError("refs must be 1-D [num_pages]")
+    return tables.shape
+
+
+def _kv_cache(k_pages, v_pages, tables, lengths, heads: int | None = None, D: int | None = None):
+    """The KvCache of checked pages [num_pages, Hkv, page_size, D] and tables."""
+    _dev(k_pages, "k_pages")
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be 4-D [num_pages, Hkv, page_size, D]")
+    if k_pages.dtype not in _DTYPES:
+        raise ValueError(f"k_pages must be float32 or bfloat16, got {k_pages.dtype}")
+    _dev(v_pages, "v_pages", k_pages.dtype)
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    pages, Hkv, ps, d = k_pages.shape
+    if heads is not None and Hkv != heads:
+        raise ValueError(f"the pages have {Hkv} heads, expected {heads}")
+    if D is not None and d != D:
+        raise ValueError(f"the pages have head size {d}, expected {D}")
+    max_seqs, max_pages = _tables2(tables, lengths)
+    return KvCache(k_pages.data_ptr(), v_pages.data_ptr(), tables.data_ptr(), lengths.data_ptr(), pages, ps, max_seqs,
+                   max_pages, _DTYPES[k_pages.dtype])
+
+
+def bl_rope_append(q=None, k=None, v=None, rope=None, cu_seqlens=None, lengths=None, seq_ids=None, k_pages=None,
+                   v_pages=None, tables=None, out_dtype=None, q_out=None, k_out=None, v_out=None, keep_kv=None,
+                   inverse: bool = False, stream=None):
+    """Rotary positions on q [T, Hq, D] and k [T, Hkv, D], rounded to out_dtype
+    (default: q's dtype), and k, v into their pages when pages are given ->
+    (q_out, k_out, v_out).  k_out and v_out are made when no pages are given
+    or keep_kv is set.  rope [positions, D] float32: cos of D/2 angles, then
+    sin.  Batch entry b's tokens are rows cu_seqlens[b] .. cu_seqlens[b+1] - 1
+    (one row each without cu_seqlens) and stand at the end of sequence
+    seq_ids[b] (default b) of lengths[seq] tokens; without lengths they stand
+    at 0, 1, ...  inverse=True rotates back (the gradient)."""
+    if q is None and k is None:
+        raise ValueError("q or k must be given")
+    first = q if q is not None else k
+    if not isinstance(first, torch.Tensor) or first.dim() != 3:
+        raise ValueError("q, k and v must be 3-D tensors [T, heads, D]")
+    T, _, D = first.shape
+    dt = first.dtype
+    qs = _rows3(q, "q", D=D, dtype=dt) if q is not None else 0
+    ks = vs = 0
+    Hkv = None
+    if (k is None) != (v is None):
+        raise ValueError("k and v must be given together")
+    if k is not None:
+        ks = _rows3(k, "k", D=D, dtype=dt, rows=T)
+        Hkv = k.shape[1]
+        vs = _rows3(v, "v", heads=Hkv, D=D, dtype=dt, rows=T)
+    Hq = q.shape[1] if q is not None else Hkv
+    Hkv = Hq if Hkv is None else Hkv
+    odt = dt if out_dtype is None else out_dtype
+    if odt not in _DTYPES:
+        raise ValueError(f"out_dtype must be float32 or bfloat16, got {odt}")
+    B = T
+    if cu_seqlens is not None:
+        _dev(cu_seqlens, "cu_seqlens", torch.int32, 2)
+        B = cu_seqlens.numel() - 1
+    if seq_ids is not None:
+        _i32(seq_ids, "seq_ids", B)
+    if rope is not None:
+        _dev(rope, "rope", torch.float32)
+        if rope.dim() != 2 or rope.shape[1] != D:
+            raise ValueError(f"rope must be [positions, {D}]")
+    cache = None
+    max_seqs = 0
+    if (k_pages is None) != (v_pages is None):
+        raise ValueError("k_pages and v_pages must be given together")
+    if k_pages is not None:
+        if k is None or tables is None or lengths is None:
+            raise ValueError("pages need k, v, tables and lengths")
+        cache = _kv_cache(k_pages, v_pages, tables, lengths, Hkv, D)
+        max_seqs = tables.shape[0]
+    elif lengths is not None:
+        _dev(lengths, "lengths", torch.int32, 1)
+        max_seqs = lengths.numel()
+    if lengths is not None and seq_ids is None and B > max_seqs:
+        raise ValueError(f"{B} batch entries, but lengths holds {max_seqs} sequences")
+    dev = first.device
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(T, Hq, D, dtype=odt, device=dev)
+        _dev(q_out, "q_out", odt, T * Hq * D)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is None and (k_out is not None or v_out is not None):
+        raise ValueError("k_out or v_out without k and v")
+    if k is not None:
+        if (cache is None) if keep_kv is None else keep_kv:
+            k_out = torch.empty(T, Hkv, D, dtype=odt, device=dev) if k_out is None else k_out
+            v_out = torch.empty(T, Hkv, D, dtype=odt, device=dev) if v_out is None else v_out
+        _opt(k_out, "k_out", odt, T * Hkv * D)
+        _opt(v_out, "v_out", odt, T * Hkv * D)
+    rc = lib().bl_rope_append(_ptr(q), _ptr(k), _ptr(v), _DTYPES[dt], qs, ks, vs, T, Hq, Hkv, D, _ptr(rope),
+                              0 if rope is None else rope.shape[0], int(inverse), _ptr(cu_seqlens), B, _ptr(seq_ids),
+                              None if cache is not None else _ptr(lengths), max_seqs,
+                              None if cache is None else ctypes.byref(cache), _ptr(q_out), _ptr(k_out), _ptr(v_out),
+                              _DTYPES[odt], _stream(stream))
+    _check(rc, "bl_rope_append")
+    return q_out, k_out, v_out
+
+
+def attn_decode_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().bl_attn_decode_workspace_bytes(B, Hq, Hkv, D))
+
+
+def bl_attn_decode(q, k_pages, v_pages, tables, lengths, seq_ids=None, window: int = 0, sinks: int = 0, scale=None,
+                   out=None, lse=None, return_lse: bool = False, workspace=None, stream=None):
+    """Attention of one new token per sequence over the paged cache -> out
+    [B, Hq, D] of q's dtype (and lse float32 [B, Hq] with return_lse=True).
+    Entry b reads sequence seq_ids[b] (default b); window = 0 sees all keys,
+    otherwise the last `window` and the first `sinks`; scale defaults to
+    D ** -0.5."""
+    qs = _rows3(q, "q")
+    B, Hq, D = q.shape
+    cache = _kv_cache(k_pages, v_pages, tables, lengths, None, D)
+    Hkv = k_pages.shape[1]
+    if seq_ids is not None:
+        _i32(seq_ids, "seq_ids", B)
+    elif B > tables.shape[0]:
+        raise ValueError(f"{B} batch entries, but the tables hold {tables.shape[0]} sequences")
+    if out is None:
+        out = torch.empty(B, Hq, D, dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(max(16, attn_decode_workspace_bytes(B, Hq, Hkv, D)), dtype=torch.uint8, device=q.device)
+    _dev(out, "out", q.dtype, B * Hq * D)
+    _opt(lse, "lse", torch.float32, B * Hq)
+    _dev(workspace, "workspace", torch.uint8)
+    rc = lib().bl_attn_decode(q.data_ptr(), _DTYPES[q.dtype], qs, B, Hq, Hkv, D, ctypes.byref(cache), _ptr(seq_ids),
+                              int(window), int(sinks), D ** -0.5 if scale is None else float(scale),
+                              workspace.data_ptr(), workspace.numel(), out.data_ptr(), _ptr(lse), _stream(stream))
+    _check(rc, "bl_attn_decode")
+    return (out, lse) if return_lse else out
+
+
+def _status(status, like):
+    if status is None:
+        return torch.empty(1, dtype=torch.int32, device=like.device)
+    return _dev(status, "status", torch.int32, 1)
+
+
+def bl_kv_extend(tables, lengths, refs, seq_ids, counts, page_size: int, status=None, stream=None):
+    """Sequence seq_ids[i] grows by counts[i] tokens: pages from the lowest free
+    ones, lengths raised -> status int32 [1] (0: done; otherwise nothing was
+    changed, see bitlinear_attn.h)."""
+    max_seqs, max_pages = _tables2(tables, lengths, refs)
+    _dev(seq_ids, "seq_ids", torch.int32, 1)
+    n = seq_ids.numel()
+    _i32(counts, "counts", n)
+    status = _status(status, tables)
+    rc = lib().bl_kv_extend(tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(), refs.numel(), page_size, max_seqs,
+                            max_pages, seq_ids.data_ptr(), counts.data_ptr(), n, status.data_ptr(), _stream(stream))
+    _check(rc, "bl_kv_extend")
+    return status
+
+
+def bl_kv_free(tables, lengths, refs, seq_ids, page_size: int, stream=None):
+    """The sequences end: their pages' refs fall by one, rows become -1, lengths 0."""
+    max_seqs, max_pages = _tables2(tables, lengths, refs)
+    _dev(seq_ids, "seq_ids", torch.int32, 1)
+    rc = lib().bl_kv_free(tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(), refs.numel(), page_size, max_seqs,
+                          max_pages, seq_ids.data_ptr(), seq_ids.numel(), _stream(stream))
+    _check(rc, "bl_kv_free")
+
+
+def _pool(pool, refs):
+    """A pool [..., num_pages, Hkv, page_size, D] -> (planes, bytes of a page, page size)."""
+    _dev(pool, "pool")
+    if pool.dim() < 4 or pool.shape[-4] != refs.numel():
+        raise ValueError("pool must be [..., num_pages, Hkv, page_size, D] with refs' number of pages")
+    if pool.dtype not in _DTYPES:
+        raise ValueError(f"pool must be float32 or bfloat16, got {pool.dtype}")
+    return math.prod(pool.shape[:-4]), math.prod(pool.shape[-3:]) * pool.element_size(), pool.shape[-2]
+
+
+def bl_kv_fork(pool, tables, lengths, refs, src, dst, status=None, workspace=None, stream=None):
+    """Sequence dst[i] (empty) becomes a copy of src[i]: full pages are shared, a
+    last partial page is copied in every plane of pool [..., num_pages, Hkv,
+    page_size, D] -> status int32 [1], as for bl_kv_extend."""
+    max_seqs, max_pages = _tables2(tables, lengths, refs)
+    planes, page_bytes, ps = _pool(pool, refs)
+    _dev(src, "src", torch.int32, 1)
+    n = src.numel()
+    _i32(dst, "dst", n)
+    status = _status(status, tables)
+    need = int(lib().bl_kv_fork_workspace_bytes(n))
+    if workspace is None:
+        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=tables.device)
+    _dev(workspace, "workspace", torch.uint8)
+    rc = lib().bl_kv_fork(pool.data_ptr(), planes, page_bytes, tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(),
+                          refs.numel(), ps, max_seqs, max_pages, src.data_ptr(), dst.data_ptr(), n,
+                          workspace.data_ptr(), workspace.numel(), status.data_ptr(), _stream(stream))
+    _check(rc, "bl_kv_fork")
+    return status
+
+
+def bl_kv_compact(pool, tables, refs, n_live=None, workspace=None, stream=None):
+    """The pages in use move to the lowest numbers, in every plane of pool;
+    tables and refs follow -> n_live int32 [1], the pages in use."""
+    max_seqs, max_pages = _tables2(tables, None, refs)
+    planes, page_bytes, _ = _pool(pool, refs)
+    if n_live is None:
+        n_live = torch.empty(1, dtype=torch.int32, device=tables.device)
+    _dev(n_live, "n_live", torch.int32, 1)
+    need = int(lib().bl_kv_compact_workspace_bytes(refs.numel()))
+    if workspace is None:
+        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=tables.device)
+    _dev(workspace, "workspace", torch.uint8)
+    rc = lib().bl_kv_compact(pool.data_ptr(), planes, page_bytes, tables.data_ptr(), refs.data_ptr(), refs.numel(),
+                             max_seqs, max_pages, workspace.data_ptr(), workspace.numel(), n_live.data_ptr(),
+                             _stream(stream))
+    _check(rc, "bl_kv_compact")
+    return n_live
+
+
+def _ragged(q, k, v, cu_q, cu_k, max_q: int, max_k: int):
+    b16 = torch.bfloat16
+    strides = [_rows3(q, "q", dtype=b16)]
+    _, Hq, D = q.shape
+    strides.append(_rows3(k, "k", D=D, dtype=b16))
+    strides.append(_rows3(v, "v", heads=k.shape[1], D=D, dtype=b16, rows=k.shape[0]))
+    _dev(cu_q, "cu_q", torch.int32, 2)
+    _i32(cu_k, "cu_k", cu_q.numel())
+    return strides, (q.shape[0], k.shape[0], Hq, k.shape[1], D), (cu_q.data_ptr(), cu_k.data_ptr(), cu_q.numel() - 1,
+                                                                 int(max_q), int(max_k))
+
+
+def bl_attn_forward(q, k, v, cu_q, cu_k, max_q: int, max_k: int, window: int = 0, sinks: int = 0, scale=None, o=None,
+                    lse=None, stream=None):
+    """Causal attention over a ragged batch, bfloat16: q [Tq, Hq, D], k, v
+    [Tk, Hkv, D]; entry b's queries are rows cu_q[b] .. cu_q[b+1] - 1 and its
+    keys cu_k[b] .. cu_k[b+1] - 1, the last query standing at the last key.
+    window = 0 sees every earlier key, otherwise the last `window` and the
+    first `sinks` -> (o bfloat16 [Tq, Hq, D], lse float32 [Hq, Tq])."""
+    (qs, ks, vs), (Tq, Tk, Hq, Hkv, D), batch = _ragged(q, k, v, cu_q, cu_k, max_q, max_k)
+    if o is None:
+        o = torch.empty(Tq, Hq, D, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty(Hq, Tq, dtype=torch.float32, device=q.device)
+    _dev(o, "o", torch.bfloat16, Tq * Hq * D)
+    _dev(lse, "lse", torch.float32, Hq * Tq)
+    rc = lib().bl_attn_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, Tq, Tk, Hq, Hkv, D, *batch,
+                               int(window), int(sinks), D ** -0.5 if scale is None else float(scale), o.data_ptr(),
+                               lse.data_ptr(), _stream(stream))
+    _check(rc, "bl_attn_forward")
+    return o, lse
+
+
+def bl_attn_backward(do, q, k, v, o, lse, cu_q, cu_k, max_q: int, max_k: int, window: int = 0, sinks: int = 0,
+                     scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of bl_attn_forward (o, lse its outputs; do bfloat16 [Tq, Hq, D])
+    -> (dq [Tq, Hq, D], dk, dv [Tk, Hkv, D]) bfloat16; dk and dv sum over the
+    query heads that share a head."""
+    (qs, ks, vs), (Tq, Tk, Hq, Hkv, D), batch = _ragged(q, k, v, cu_q, cu_k, max_q, max_k)
+    dos = _rows3(do, "do", heads=Hq, D=D, dtype=torch.bfloat16, rows=Tq)
+    _dev(o, "o", torch.bfloat16, Tq * Hq * D)
+    _dev(lse, "lse", torch.float32, Hq * Tq)
+    if dq is None:
+        dq = torch.empty(Tq, Hq, D, dtype=torch.bfloat16, device=q.device)
+    if dk is None:
+        dk = torch.empty(Tk, Hkv, D, dtype=torch.bfloat16, device=q.device)
+    if dv is None:
+        dv = torch.empty(Tk, Hkv, D, dtype=torch.bfloat16, device=q.device)
+    _dev(dq, "dq", torch.bfloat16, Tq * Hq * D)
+    _dev(dk, "dk", torch.bfloat16, Tk * Hkv * D)
+    _dev(dv, "dv", torch.bfloat16, Tk * Hkv * D)
+    need = int(lib().bl_attn_backward_workspace_bytes(Tq, Tk, Hq, Hkv, D, batch[2], batch[3], batch[4], int(window),
+                                                      int(sinks)))
+    if workspace is None:
+        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
+    _dev(workspace, "workspace", torch.uint8)
+    rc = lib().bl_attn_backward(do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                dos, qs, ks, vs, Tq, Tk, Hq, Hkv, D, *batch, int(window), int(sinks),
+                                D ** -0.5 if scale is None else float(scale), workspace.data_ptr(), workspace.numel(),
+                                dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _stream(stream))
+    _check(rc, "bl_attn_backward")
+    return dq, dk, dv
 
 
 def bl_debug_decode_plan(shapes, M: int, sms: int = 148):

@@ -21,6 +21,11 @@
 
 using namespace bl;
 
+namespace bl {
+// attention.cu: reads and clears that translation unit's device error word
+bool attn_take_device_error(u32 *out);
+}  // namespace bl
+
 namespace {
 
 constexpr int BL_VERSION = 100;
@@ -486,6 +491,7 @@ const char *bl_status_string(bl_status s) {
         case BL_ERR_TIMEOUT: return "BL_ERR_TIMEOUT: a bounded device-side wait gave up";
         case BL_ERR_WORKSPACE: return "BL_ERR_WORKSPACE: workspace missing or too small";
         case BL_ERR_DEVICE: return "BL_ERR_DEVICE: current device is not compute capability 10.x";
+        case BL_ERR_INDEX: return "BL_ERR_INDEX: an index in device memory lies outside its array";
     }
     return "BL_ERR_UNKNOWN";
 }
@@ -497,7 +503,11 @@ bl_status bl_check_device_error(bl_stream_t stream) {
     u32 v = 0, zero = 0;
     if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(v)) != cudaSuccess) return BL_ERR_CUDA;
     if (v != 0 && cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero)) != cudaSuccess) return BL_ERR_CUDA;
-    return v ? BL_ERR_TIMEOUT : BL_OK;
+    u32 a = 0;  // the attention kernels' word (their own translation unit)
+    if (!attn_take_device_error(&a)) return BL_ERR_CUDA;
+    v |= a;
+    if (v & ~(u32)DEVERR_INDEX) return BL_ERR_TIMEOUT;
+    return v ? BL_ERR_INDEX : BL_OK;
 }
 
 size_t bl_quant_weights_workspace_bytes(int64_t N, int64_t K) {

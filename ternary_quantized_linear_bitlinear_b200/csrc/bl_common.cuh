@@ -21,6 +21,7 @@ enum : u32 {
     DEVERR_TIMEOUT_EXPAND = 1u << 2,
     DEVERR_TIMEOUT_EPILOGUE = 1u << 3,
     DEVERR_TMEM_ALLOC = 1u << 4,
+    DEVERR_INDEX = 1u << 5,  // an index read from device memory was outside its array
 };
 
 __device__ u32 g_device_error;
@@ -44,6 +45,20 @@ __device__ __forceinline__ uint4 ldg_stream_v4(const void *p) {
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                  : "l"(p));
+    return r;
+}
+
+// Two floats rounded to bfloat16 (nearest, ties to even), `lo` in the low half.
+__device__ __forceinline__ u32 pack_bf16(float lo, float hi) {
+    u32 r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 2^x, at most 2 ulp off over the full range (subnormal results are 0).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
