@@ -5,6 +5,7 @@
 // launch and enqueues it on the caller's stream.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstring>
 #include <mutex>
 
@@ -33,8 +34,6 @@ namespace {
 constexpr int MAX_DEVICES = 64;
 constexpr int64_t I32_MAX = 0x7fffffffLL;
 constexpr float LOG2E = 1.44269504088896f;
-// CTAs of a single-token attention launch at most (the workspace is sized for them)
-constexpr int AD_MAX_CTAS = 640;
 
 struct AttnDevice {
     bool init = false, ok = false;
@@ -145,15 +144,22 @@ inline void head_groups(int64_t group, int *parts, int *gsize) {
     *gsize = (int)((group + *parts - 1) / *parts);
 }
 
-template <bool BF16, int DP, int G, int WARPS, int OCC>
+template <bool BF16, int DP, int G, int WARPS, int OCC, int SLOTS>
 bl_status launch_decode(DecodeAttnParams &P, const AttnDevice &d, int64_t batches_at_most, cudaStream_t st) {
     int ctas = d.sms * OCC;
     if (ctas > AD_MAX_CTAS) ctas = AD_MAX_CTAS;
-    // no piece is smaller than one batch per warp
-    const int64_t pieces = (batches_at_most + WARPS - 1) / WARPS;
-    if (pieces < ctas) ctas = (int)(pieces < 1 ? 1 : pieces);
-    const size_t smem = (size_t)WARPS * G * (DP + 2) * 4;
-    k_attn_decode<BF16, DP, G, WARPS, OCC><<<ctas, WARPS * 32, smem, st>>>(P);
+    // no more warps than batches
+    const int64_t need = (batches_at_most + WARPS - 1) / WARPS;
+    if (need < ctas) ctas = (int)(need < 1 ? 1 : need);
+    constexpr int smem = ad_smem(WARPS, G, DP, SLOTS);
+    static std::atomic<u64> ready{0};  // devices this kernel's shared memory is set up on
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return BL_ERR_CUDA;
+    if (!(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
+        if (!big_smem(k_attn_decode<BF16, DP, G, WARPS, OCC, SLOTS>, smem)) return BL_ERR_CUDA;
+        ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    k_attn_decode<BF16, DP, G, WARPS, OCC, SLOTS><<<ctas, WARPS * 32, smem, st>>>(P);
     if (cudaGetLastError() != cudaSuccess) return BL_ERR_CUDA;
     return launch_after(k_attn_join<DP>, dim3((unsigned)P.B, (unsigned)(P.Hkv * P.parts)), AD_JOIN_THREADS, 0, st, P,
                         ctas, WARPS);
@@ -161,13 +167,14 @@ bl_status launch_decode(DecodeAttnParams &P, const AttnDevice &d, int64_t batche
 
 template <bool BF16, int DP>
 bl_status decode_by_heads(DecodeAttnParams &P, const AttnDevice &d, int64_t batches, cudaStream_t st) {
-    // shared memory of the merge stays below 48 KiB for every choice
+    // two CTAs of eight warps an SM with three slots each where registers and
+    // shared memory allow it
     switch (P.gsize) {
-        case 1: return launch_decode<BF16, DP, 1, 8, 2>(P, d, batches, st);
-        case 2: return launch_decode<BF16, DP, 2, 8, 2>(P, d, batches, st);
-        case 3: return launch_decode<BF16, DP, 3, 8, 1>(P, d, batches, st);
-        case 4: return launch_decode<BF16, DP, 4, 8, 1>(P, d, batches, st);
-        default: return launch_decode<BF16, DP, 8, 8, 1>(P, d, batches, st);
+        case 1: return launch_decode<BF16, DP, 1, 8, 2, 3>(P, d, batches, st);
+        case 2: return launch_decode<BF16, DP, 2, 8, 2, 3>(P, d, batches, st);
+        case 3: return launch_decode<BF16, DP, 3, 8, 2, 3>(P, d, batches, st);
+        case 4: return launch_decode<BF16, DP, 4, 7, 2, 3>(P, d, batches, st);
+        default: return launch_decode<BF16, DP, 8, 8, 1, 4>(P, d, batches, st);
     }
 }
 
