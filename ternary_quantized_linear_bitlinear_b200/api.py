@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -70,6 +71,11 @@ class KvCache(ctypes.Structure):
                 ("page_size", _i64), ("max_seqs", _i64), ("max_pages", _i64), ("dtype", _int)]
 
 
+# The same bytes without a Structure object per call (a fifth of its cost).
+_KV_CACHE = struct.Struct("PPPPqqqqi4x")
+assert _KV_CACHE.size == ctypes.sizeof(KvCache)
+
+
 _SIGS = {
     "bl_status_string": (ctypes.c_char_p, [_int]),
     "bl_version": (_int, []),
@@ -98,9 +104,9 @@ _SIGS = {
     "bl_linear_grouped": (_int, [ctypes.POINTER(LinearProblem), _int, _int, _p, _int, _i64, _i64, _p, _f32, _p, _sz,
                                  _p]),
     "bl_rope_append": (_int, [_p, _p, _p, _int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _p, _i64, _int, _p, _i64, _p,
-                              _p, _i64, ctypes.POINTER(KvCache), _p, _p, _p, _int, _p]),
+                              _p, _i64, _p, _p, _p, _p, _int, _p]),
     "bl_attn_decode_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
-    "bl_attn_decode": (_int, [_p, _int, _i64, _i64, _i64, _i64, _i64, ctypes.POINTER(KvCache), _p, _i64, _i64, _f32, _p,
+    "bl_attn_decode": (_int, [_p, _int, _i64, _i64, _i64, _i64, _i64, _p, _p, _i64, _i64, _f32, _p,
                               _sz, _p, _p, _p]),
     "bl_kv_extend": (_int, [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _p]),
     "bl_kv_free": (_int, [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _i64, _p]),
@@ -155,7 +161,8 @@ def _stream(stream) -> int:
     """Raw handle of `stream` (default: torch's current stream).  The library
     launches on the current device, so an explicit stream must belong to it."""
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle of torch.cuda.current_stream(), without building the Stream object (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(_current_device())
     if stream.device_index != _current_device():
         raise ValueError(f"stream belongs to cuda:{stream.device_index}, the current device is "
                          f"cuda:{_current_device()}")
@@ -581,10 +588,30 @@ def bl_linear_grouped(Ws, X, subln_gain=None, subln_eps: float = 1e-6, Ys=None, 
 
 
 # -- attention and its cache (include/bitlinear_attn.h) ------------------------
+#
+# These calls are a few microseconds of GPU work at decode sizes, so a valid
+# buffer is recognised by one expression (_ok, _ok3) and only a doubtful one
+# goes through the checks that say what is wrong with it.
 
-def _rows3(t, name: str, heads: int | None = None, D: int | None = None, dtype=None, rows: int | None = None):
+_Tensor = torch.Tensor
+
+
+def _ok(t, dtype, cur: int) -> bool:
+    return isinstance(t, _Tensor) and t.is_cuda and t.get_device() == cur and t.dtype is dtype and t.is_contiguous()
+
+
+def _rows3(t, name: str, cur: int, heads: int | None = None, D: int | None = None, dtype=None, rows: int | None = None):
     """Rows of heads [T, H, D] on the current device whose heads are contiguous
     (a row may be part of a wider one) -> row stride in elements."""
+    if isinstance(t, _Tensor) and t.is_cuda and t.get_device() == cur and t.dim() == 3 and t.dtype in _DTYPES:
+        T, H, d = t.shape
+        st, sh, sd = t.stride()
+        if ((dtype is None or t.dtype is dtype) and (rows is None or T == rows) and (heads is None or H == heads)
+                and (D is None or d == D) and sd == 1 and (sh == d or H == 1)):
+            if T == 1:
+                return H * d
+            if st >= H * d:
+                return st
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 3:
@@ -609,44 +636,60 @@ def _rows3(t, name: str, heads: int | None = None, D: int | None = None, dtype=N
     return stride
 
 
-def _i32(t, name: str, numel: int):
-    _dev(t, name, torch.int32)
-    if t.numel() != numel:
-        raise ValueError(f"{name} holds {t.numel()} elements, expected {numel}")
-    return t
+def _buf(t, name: str, dtype, min_numel: int, cur: int):
+    if not (_ok(t, dtype, cur) and t.numel() >= min_numel):
+        _dev(t, name, dtype, min_numel)
+    return t.data_ptr()
 
 
-def _tables2(tables, lengths, refs=None):
-    _dev(tables, "tables", torch.int32)
-    if tables.dim() != 2:
-        raise ValueError("tables must be 2-D [max_seqs, max_pages]")
+def _i32(t, name: str, numel: int, cur: int):
+    """An int32 buffer of exactly numel elements -> its address."""
+    if not (_ok(t, torch.int32, cur) and t.numel() == numel):
+        _dev(t, name, torch.int32)
+        if t.numel() != numel:
+            raise ValueError(f"{name} holds {t.numel()} elements, expected {numel}")
+    return t.data_ptr()
+
+
+def _tables2(tables, lengths, refs, cur: int):
+    """Checked tables [max_seqs, max_pages], lengths [max_seqs] and refs
+    [num_pages] (either may be None) -> (max_seqs, max_pages)."""
+    if not (_ok(tables, torch.int32, cur) and tables.dim() == 2):
+        _dev(tables, "tables", torch.int32)
+        if tables.dim() != 2:
+            raise ValueError("tables must be 2-D [max_seqs, max_pages]")
+    max_seqs, max_pages = tables.shape
     if lengths is not None:
-        _i32(lengths, "lengths", tables.shape[0])
-    if refs is not None:
+        _i32(lengths, "lengths", max_seqs, cur)
+    if refs is not None and not (_ok(refs, torch.int32, cur) and refs.dim() == 1):
         _dev(refs, "refs", torch.int32)
         if refs.dim() != 1:
             raise ValueError("refs must be 1-D [num_pages]")
-    return tables.shape
+    return max_seqs, max_pages
 
 
-def _kv_cache(k_pages, v_pages, tables, lengths, heads: int | None = None, D: int | None = None):
-    """The KvCache of checked pages [num_pages, Hkv, page_size, D] and tables."""
-    _dev(k_pages, "k_pages")
-    if k_pages.dim() != 4:
-        raise ValueError("k_pages must be 4-D [num_pages, Hkv, page_size, D]")
-    if k_pages.dtype not in _DTYPES:
-        raise ValueError(f"k_pages must be float32 or bfloat16, got {k_pages.dtype}")
-    _dev(v_pages, "v_pages", k_pages.dtype)
-    if v_pages.shape != k_pages.shape:
-        raise ValueError("k_pages and v_pages must have the same shape")
+def _kv_cache(k_pages, v_pages, tables, lengths, heads, D: int, cur: int):
+    """The bytes of a bl_kv_cache of checked pages [num_pages, Hkv, page_size, D]
+    and tables -> (bytes, Hkv, max_seqs)."""
+    dt = k_pages.dtype if isinstance(k_pages, _Tensor) else None
+    if not (dt in _DTYPES and _ok(k_pages, dt, cur) and _ok(v_pages, dt, cur) and k_pages.dim() == 4
+            and v_pages.shape == k_pages.shape):
+        _dev(k_pages, "k_pages")
+        if k_pages.dim() != 4:
+            raise ValueError("k_pages must be 4-D [num_pages, Hkv, page_size, D]")
+        if dt not in _DTYPES:
+            raise ValueError(f"k_pages must be float32 or bfloat16, got {dt}")
+        _dev(v_pages, "v_pages", dt)
+        if v_pages.shape != k_pages.shape:
+            raise ValueError("k_pages and v_pages must have the same shape")
     pages, Hkv, ps, d = k_pages.shape
     if heads is not None and Hkv != heads:
         raise ValueError(f"the pages have {Hkv} heads, expected {heads}")
-    if D is not None and d != D:
+    if d != D:
         raise ValueError(f"the pages have head size {d}, expected {D}")
-    max_seqs, max_pages = _tables2(tables, lengths)
-    return KvCache(k_pages.data_ptr(), v_pages.data_ptr(), tables.data_ptr(), lengths.data_ptr(), pages, ps, max_seqs,
-                   max_pages, _DTYPES[k_pages.dtype])
+    max_seqs, max_pages = _tables2(tables, lengths, None, cur)
+    return _KV_CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), tables.data_ptr(), lengths.data_ptr(), pages, ps,
+                          max_seqs, max_pages, _DTYPES[dt]), Hkv, max_seqs
 
 
 def bl_rope_append(q=None, k=None, v=None, rope=None, cu_seqlens=None, lengths=None, seq_ids=None, k_pages=None,
@@ -659,38 +702,39 @@ def bl_rope_append(q=None, k=None, v=None, rope=None, cu_seqlens=None, lengths=N
     sin.  Batch entry b's tokens are rows cu_seqlens[b] .. cu_seqlens[b+1] - 1
     (one row each without cu_seqlens) and stand at the end of sequence
     seq_ids[b] (default b) of lengths[seq] tokens; without lengths they stand
-    at 0, 1, ...  inverse=True rotates back (the gradient)."""
-    if q is None and k is None:
-        raise ValueError("q or k must be given")
+    at 0, 1, ...  inverse=True rotates back (the gradient).  An output may be
+    the very tensor it comes from (same dtype, same rows), not overlap it
+    otherwise."""
+    cur = _current_device()
     first = q if q is not None else k
-    if not isinstance(first, torch.Tensor) or first.dim() != 3:
+    if first is None:
+        raise ValueError("q or k must be given")
+    if not isinstance(first, _Tensor) or first.dim() != 3:
         raise ValueError("q, k and v must be 3-D tensors [T, heads, D]")
-    T, _, D = first.shape
+    T, Hq, D = first.shape
     dt = first.dtype
-    qs = _rows3(q, "q", D=D, dtype=dt) if q is not None else 0
-    ks = vs = 0
-    Hkv = None
+    qs = ks = vs = 0
+    if q is not None:
+        qs = _rows3(q, "q", cur, dtype=dt)
+    Hkv = Hq
     if (k is None) != (v is None):
         raise ValueError("k and v must be given together")
     if k is not None:
-        ks = _rows3(k, "k", D=D, dtype=dt, rows=T)
+        ks = _rows3(k, "k", cur, D=D, dtype=dt, rows=T)
         Hkv = k.shape[1]
-        vs = _rows3(v, "v", heads=Hkv, D=D, dtype=dt, rows=T)
-    Hq = q.shape[1] if q is not None else Hkv
-    Hkv = Hq if Hkv is None else Hkv
+        vs = _rows3(v, "v", cur, heads=Hkv, D=D, dtype=dt, rows=T)
     odt = dt if out_dtype is None else out_dtype
     if odt not in _DTYPES:
         raise ValueError(f"out_dtype must be float32 or bfloat16, got {odt}")
     B = T
     if cu_seqlens is not None:
-        _dev(cu_seqlens, "cu_seqlens", torch.int32, 2)
+        _buf(cu_seqlens, "cu_seqlens", torch.int32, 2, cur)
         B = cu_seqlens.numel() - 1
     if seq_ids is not None:
-        _i32(seq_ids, "seq_ids", B)
-    if rope is not None:
+        _i32(seq_ids, "seq_ids", B, cur)
+    if rope is not None and not (_ok(rope, torch.float32, cur) and rope.dim() == 2 and rope.shape[1] == D):
         _dev(rope, "rope", torch.float32)
-        if rope.dim() != 2 or rope.shape[1] != D:
-            raise ValueError(f"rope must be [positions, {D}]")
+        raise ValueError(f"rope must be [positions, {D}]")
     cache = None
     max_seqs = 0
     if (k_pages is None) != (v_pages is None):
@@ -698,34 +742,36 @@ def bl_rope_append(q=None, k=None, v=None, rope=None, cu_seqlens=None, lengths=N
     if k_pages is not None:
         if k is None or tables is None or lengths is None:
             raise ValueError("pages need k, v, tables and lengths")
-        cache = _kv_cache(k_pages, v_pages, tables, lengths, Hkv, D)
-        max_seqs = tables.shape[0]
+        cache, _, max_seqs = _kv_cache(k_pages, v_pages, tables, lengths, Hkv, D, cur)
     elif lengths is not None:
-        _dev(lengths, "lengths", torch.int32, 1)
+        _buf(lengths, "lengths", torch.int32, 1, cur)
         max_seqs = lengths.numel()
     if lengths is not None and seq_ids is None and B > max_seqs:
         raise ValueError(f"{B} batch entries, but lengths holds {max_seqs} sequences")
-    dev = first.device
     if q is not None:
         if q_out is None:
-            q_out = torch.empty(T, Hq, D, dtype=odt, device=dev)
-        _dev(q_out, "q_out", odt, T * Hq * D)
+            q_out = torch.empty((T, Hq, D), dtype=odt, device=q.device)
+        else:
+            _buf(q_out, "q_out", odt, T * Hq * D, cur)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if k is None and (k_out is not None or v_out is not None):
-        raise ValueError("k_out or v_out without k and v")
-    if k is not None:
+    if k is None:
+        if k_out is not None or v_out is not None:
+            raise ValueError("k_out or v_out without k and v")
+    else:
         if (cache is None) if keep_kv is None else keep_kv:
-            k_out = torch.empty(T, Hkv, D, dtype=odt, device=dev) if k_out is None else k_out
-            v_out = torch.empty(T, Hkv, D, dtype=odt, device=dev) if v_out is None else v_out
-        _opt(k_out, "k_out", odt, T * Hkv * D)
-        _opt(v_out, "v_out", odt, T * Hkv * D)
+            k_out = torch.empty((T, Hkv, D), dtype=odt, device=k.device) if k_out is None else k_out
+            v_out = torch.empty((T, Hkv, D), dtype=odt, device=k.device) if v_out is None else v_out
+        if k_out is not None:
+            _buf(k_out, "k_out", odt, T * Hkv * D, cur)
+        if v_out is not None:
+            _buf(v_out, "v_out", odt, T * Hkv * D, cur)
     rc = lib().bl_rope_append(_ptr(q), _ptr(k), _ptr(v), _DTYPES[dt], qs, ks, vs, T, Hq, Hkv, D, _ptr(rope),
                               0 if rope is None else rope.shape[0], int(inverse), _ptr(cu_seqlens), B, _ptr(seq_ids),
-                              None if cache is not None else _ptr(lengths), max_seqs,
-                              None if cache is None else ctypes.byref(cache), _ptr(q_out), _ptr(k_out), _ptr(v_out),
-                              _DTYPES[odt], _stream(stream))
-    _check(rc, "bl_rope_append")
+                              None if cache is not None else _ptr(lengths), max_seqs, cache, _ptr(q_out), _ptr(k_out),
+                              _ptr(v_out), _DTYPES[odt], _stream(stream))
+    if rc:
+        _check(rc, "bl_rope_append")
     return q_out, k_out, v_out
 
 
@@ -739,121 +785,143 @@ def bl_attn_decode(q, k_pages, v_pages, tables, lengths, seq_ids=None, window: i
     [B, Hq, D] of q's dtype (and lse float32 [B, Hq] with return_lse=True).
     Entry b reads sequence seq_ids[b] (default b); window = 0 sees all keys,
     otherwise the last `window` and the first `sinks`; scale defaults to
-    D ** -0.5."""
-    qs = _rows3(q, "q")
+    D ** -0.5.  Calls that may run at the same time need workspaces of their
+    own (the default: a new one per call)."""
+    cur = _current_device()
+    qs = _rows3(q, "q", cur)
     B, Hq, D = q.shape
-    cache = _kv_cache(k_pages, v_pages, tables, lengths, None, D)
-    Hkv = k_pages.shape[1]
+    cache, Hkv, max_seqs = _kv_cache(k_pages, v_pages, tables, lengths, None, D, cur)
     if seq_ids is not None:
-        _i32(seq_ids, "seq_ids", B)
-    elif B > tables.shape[0]:
-        raise ValueError(f"{B} batch entries, but the tables hold {tables.shape[0]} sequences")
+        _i32(seq_ids, "seq_ids", B, cur)
+    elif B > max_seqs:
+        raise ValueError(f"{B} batch entries, but the tables hold {max_seqs} sequences")
+    dev = q.device
     if out is None:
-        out = torch.empty(B, Hq, D, dtype=q.dtype, device=q.device)
-    if lse is None and return_lse:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        out = torch.empty((B, Hq, D), dtype=q.dtype, device=dev)
+    else:
+        _buf(out, "out", q.dtype, B * Hq * D, cur)
+    if lse is not None:
+        _buf(lse, "lse", torch.float32, B * Hq, cur)
+    elif return_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    L = lib()
     if workspace is None:
-        workspace = torch.empty(max(16, attn_decode_workspace_bytes(B, Hq, Hkv, D)), dtype=torch.uint8, device=q.device)
-    _dev(out, "out", q.dtype, B * Hq * D)
-    _opt(lse, "lse", torch.float32, B * Hq)
-    _dev(workspace, "workspace", torch.uint8)
-    rc = lib().bl_attn_decode(q.data_ptr(), _DTYPES[q.dtype], qs, B, Hq, Hkv, D, ctypes.byref(cache), _ptr(seq_ids),
-                              int(window), int(sinks), D ** -0.5 if scale is None else float(scale),
-                              workspace.data_ptr(), workspace.numel(), out.data_ptr(), _ptr(lse), _stream(stream))
-    _check(rc, "bl_attn_decode")
+        workspace = torch.empty(L.bl_attn_decode_workspace_bytes(B, Hq, Hkv, D) or 16, dtype=torch.uint8, device=dev)
+    else:
+        _buf(workspace, "workspace", torch.uint8, 1, cur)
+    rc = L.bl_attn_decode(q.data_ptr(), _DTYPES[q.dtype], qs, B, Hq, Hkv, D, cache, _ptr(seq_ids), window, sinks,
+                          D ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.numel(),
+                          out.data_ptr(), _ptr(lse), _stream(stream))
+    if rc:
+        _check(rc, "bl_attn_decode")
     return (out, lse) if return_lse else out
 
 
-def _status(status, like):
+def _status(status, like, cur: int):
     if status is None:
         return torch.empty(1, dtype=torch.int32, device=like.device)
-    return _dev(status, "status", torch.int32, 1)
+    _buf(status, "status", torch.int32, 1, cur)
+    return status
 
 
 def bl_kv_extend(tables, lengths, refs, seq_ids, counts, page_size: int, status=None, stream=None):
     """Sequence seq_ids[i] grows by counts[i] tokens: pages from the lowest free
     ones, lengths raised -> status int32 [1] (0: done; otherwise nothing was
     changed, see bitlinear_attn.h)."""
-    max_seqs, max_pages = _tables2(tables, lengths, refs)
-    _dev(seq_ids, "seq_ids", torch.int32, 1)
+    cur = _current_device()
+    max_seqs, max_pages = _tables2(tables, lengths, refs, cur)
+    ids = _buf(seq_ids, "seq_ids", torch.int32, 1, cur)
     n = seq_ids.numel()
-    _i32(counts, "counts", n)
-    status = _status(status, tables)
+    cnt = _i32(counts, "counts", n, cur)
+    status = _status(status, tables, cur)
     rc = lib().bl_kv_extend(tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(), refs.numel(), page_size, max_seqs,
-                            max_pages, seq_ids.data_ptr(), counts.data_ptr(), n, status.data_ptr(), _stream(stream))
-    _check(rc, "bl_kv_extend")
+                            max_pages, ids, cnt, n, status.data_ptr(), _stream(stream))
+    if rc:
+        _check(rc, "bl_kv_extend")
     return status
 
 
 def bl_kv_free(tables, lengths, refs, seq_ids, page_size: int, stream=None):
     """The sequences end: their pages' refs fall by one, rows become -1, lengths 0."""
-    max_seqs, max_pages = _tables2(tables, lengths, refs)
-    _dev(seq_ids, "seq_ids", torch.int32, 1)
+    cur = _current_device()
+    max_seqs, max_pages = _tables2(tables, lengths, refs, cur)
+    ids = _buf(seq_ids, "seq_ids", torch.int32, 1, cur)
     rc = lib().bl_kv_free(tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(), refs.numel(), page_size, max_seqs,
-                          max_pages, seq_ids.data_ptr(), seq_ids.numel(), _stream(stream))
-    _check(rc, "bl_kv_free")
+                          max_pages, ids, seq_ids.numel(), _stream(stream))
+    if rc:
+        _check(rc, "bl_kv_free")
 
 
-def _pool(pool, refs):
+def _pool(pool, refs, cur: int):
     """A pool [..., num_pages, Hkv, page_size, D] -> (planes, bytes of a page, page size)."""
-    _dev(pool, "pool")
-    if pool.dim() < 4 or pool.shape[-4] != refs.numel():
+    dt = pool.dtype if isinstance(pool, _Tensor) else None
+    if not (dt in _DTYPES and _ok(pool, dt, cur)):
+        _dev(pool, "pool")
+        if dt not in _DTYPES:
+            raise ValueError(f"pool must be float32 or bfloat16, got {dt}")
+    shape = pool.shape
+    if len(shape) < 4 or shape[-4] != refs.numel():
         raise ValueError("pool must be [..., num_pages, Hkv, page_size, D] with refs' number of pages")
-    if pool.dtype not in _DTYPES:
-        raise ValueError(f"pool must be float32 or bfloat16, got {pool.dtype}")
-    return math.prod(pool.shape[:-4]), math.prod(pool.shape[-3:]) * pool.element_size(), pool.shape[-2]
+    return math.prod(shape[:-4]), shape[-3] * shape[-2] * shape[-1] * pool.element_size(), shape[-2]
 
 
 def bl_kv_fork(pool, tables, lengths, refs, src, dst, status=None, workspace=None, stream=None):
     """Sequence dst[i] (empty) becomes a copy of src[i]: full pages are shared, a
     last partial page is copied in every plane of pool [..., num_pages, Hkv,
     page_size, D] -> status int32 [1], as for bl_kv_extend."""
-    max_seqs, max_pages = _tables2(tables, lengths, refs)
-    planes, page_bytes, ps = _pool(pool, refs)
-    _dev(src, "src", torch.int32, 1)
+    cur = _current_device()
+    max_seqs, max_pages = _tables2(tables, lengths, refs, cur)
+    planes, page_bytes, ps = _pool(pool, refs, cur)
+    a = _buf(src, "src", torch.int32, 1, cur)
     n = src.numel()
-    _i32(dst, "dst", n)
-    status = _status(status, tables)
-    need = int(lib().bl_kv_fork_workspace_bytes(n))
+    b = _i32(dst, "dst", n, cur)
+    status = _status(status, tables, cur)
+    L = lib()
     if workspace is None:
-        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=tables.device)
-    _dev(workspace, "workspace", torch.uint8)
-    rc = lib().bl_kv_fork(pool.data_ptr(), planes, page_bytes, tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(),
-                          refs.numel(), ps, max_seqs, max_pages, src.data_ptr(), dst.data_ptr(), n,
-                          workspace.data_ptr(), workspace.numel(), status.data_ptr(), _stream(stream))
-    _check(rc, "bl_kv_fork")
+        workspace = torch.empty(L.bl_kv_fork_workspace_bytes(n) or 16, dtype=torch.uint8, device=tables.device)
+    else:
+        _buf(workspace, "workspace", torch.uint8, 1, cur)
+    rc = L.bl_kv_fork(pool.data_ptr(), planes, page_bytes, tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(),
+                      refs.numel(), ps, max_seqs, max_pages, a, b, n, workspace.data_ptr(), workspace.numel(),
+                      status.data_ptr(), _stream(stream))
+    if rc:
+        _check(rc, "bl_kv_fork")
     return status
 
 
 def bl_kv_compact(pool, tables, refs, n_live=None, workspace=None, stream=None):
     """The pages in use move to the lowest numbers, in every plane of pool;
     tables and refs follow -> n_live int32 [1], the pages in use."""
-    max_seqs, max_pages = _tables2(tables, None, refs)
-    planes, page_bytes, _ = _pool(pool, refs)
+    cur = _current_device()
+    max_seqs, max_pages = _tables2(tables, None, refs, cur)
+    planes, page_bytes, _ = _pool(pool, refs, cur)
     if n_live is None:
         n_live = torch.empty(1, dtype=torch.int32, device=tables.device)
-    _dev(n_live, "n_live", torch.int32, 1)
-    need = int(lib().bl_kv_compact_workspace_bytes(refs.numel()))
+    else:
+        _buf(n_live, "n_live", torch.int32, 1, cur)
+    L = lib()
+    pages = refs.numel()
     if workspace is None:
-        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=tables.device)
-    _dev(workspace, "workspace", torch.uint8)
-    rc = lib().bl_kv_compact(pool.data_ptr(), planes, page_bytes, tables.data_ptr(), refs.data_ptr(), refs.numel(),
-                             max_seqs, max_pages, workspace.data_ptr(), workspace.numel(), n_live.data_ptr(),
-                             _stream(stream))
-    _check(rc, "bl_kv_compact")
+        workspace = torch.empty(L.bl_kv_compact_workspace_bytes(pages) or 16, dtype=torch.uint8, device=tables.device)
+    else:
+        _buf(workspace, "workspace", torch.uint8, 1, cur)
+    rc = L.bl_kv_compact(pool.data_ptr(), planes, page_bytes, tables.data_ptr(), refs.data_ptr(), pages, max_seqs,
+                         max_pages, workspace.data_ptr(), workspace.numel(), n_live.data_ptr(), _stream(stream))
+    if rc:
+        _check(rc, "bl_kv_compact")
     return n_live
 
 
-def _ragged(q, k, v, cu_q, cu_k, max_q: int, max_k: int):
+def _ragged(q, k, v, cu_q, cu_k, cur: int):
     b16 = torch.bfloat16
-    strides = [_rows3(q, "q", dtype=b16)]
-    _, Hq, D = q.shape
-    strides.append(_rows3(k, "k", D=D, dtype=b16))
-    strides.append(_rows3(v, "v", heads=k.shape[1], D=D, dtype=b16, rows=k.shape[0]))
-    _dev(cu_q, "cu_q", torch.int32, 2)
-    _i32(cu_k, "cu_k", cu_q.numel())
-    return strides, (q.shape[0], k.shape[0], Hq, k.shape[1], D), (cu_q.data_ptr(), cu_k.data_ptr(), cu_q.numel() - 1,
-                                                                 int(max_q), int(max_k))
+    qs = _rows3(q, "q", cur, dtype=b16)
+    Tq, Hq, D = q.shape
+    ks = _rows3(k, "k", cur, D=D, dtype=b16)
+    Tk, Hkv, _ = k.shape
+    vs = _rows3(v, "v", cur, heads=Hkv, D=D, dtype=b16, rows=Tk)
+    a = _buf(cu_q, "cu_q", torch.int32, 2, cur)
+    n = cu_q.numel()
+    return (qs, ks, vs), (Tq, Tk, Hq, Hkv, D), (a, _i32(cu_k, "cu_k", n, cur), n - 1)
 
 
 def bl_attn_forward(q, k, v, cu_q, cu_k, max_q: int, max_k: int, window: int = 0, sinks: int = 0, scale=None, o=None,
@@ -863,17 +931,21 @@ def bl_attn_forward(q, k, v, cu_q, cu_k, max_q: int, max_k: int, window: int = 0
     keys cu_k[b] .. cu_k[b+1] - 1, the last query standing at the last key.
     window = 0 sees every earlier key, otherwise the last `window` and the
     first `sinks` -> (o bfloat16 [Tq, Hq, D], lse float32 [Hq, Tq])."""
-    (qs, ks, vs), (Tq, Tk, Hq, Hkv, D), batch = _ragged(q, k, v, cu_q, cu_k, max_q, max_k)
+    cur = _current_device()
+    strides, (Tq, Tk, Hq, Hkv, D), (a, b, B) = _ragged(q, k, v, cu_q, cu_k, cur)
     if o is None:
-        o = torch.empty(Tq, Hq, D, dtype=torch.bfloat16, device=q.device)
+        o = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _buf(o, "o", torch.bfloat16, Tq * Hq * D, cur)
     if lse is None:
-        lse = torch.empty(Hq, Tq, dtype=torch.float32, device=q.device)
-    _dev(o, "o", torch.bfloat16, Tq * Hq * D)
-    _dev(lse, "lse", torch.float32, Hq * Tq)
-    rc = lib().bl_attn_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, Tq, Tk, Hq, Hkv, D, *batch,
-                               int(window), int(sinks), D ** -0.5 if scale is None else float(scale), o.data_ptr(),
+        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
+    else:
+        _buf(lse, "lse", torch.float32, Hq * Tq, cur)
+    rc = lib().bl_attn_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, Tq, Tk, Hq, Hkv, D, a, b, B, max_q,
+                               max_k, window, sinks, D ** -0.5 if scale is None else scale, o.data_ptr(),
                                lse.data_ptr(), _stream(stream))
-    _check(rc, "bl_attn_forward")
+    if rc:
+        _check(rc, "bl_attn_forward")
     return o, lse
 
 
@@ -882,29 +954,37 @@ def bl_attn_backward(do, q, k, v, o, lse, cu_q, cu_k, max_q: int, max_k: int, wi
     """Gradients of bl_attn_forward (o, lse its outputs; do bfloat16 [Tq, Hq, D])
     -> (dq [Tq, Hq, D], dk, dv [Tk, Hkv, D]) bfloat16; dk and dv sum over the
     query heads that share a head."""
-    (qs, ks, vs), (Tq, Tk, Hq, Hkv, D), batch = _ragged(q, k, v, cu_q, cu_k, max_q, max_k)
-    dos = _rows3(do, "do", heads=Hq, D=D, dtype=torch.bfloat16, rows=Tq)
-    _dev(o, "o", torch.bfloat16, Tq * Hq * D)
-    _dev(lse, "lse", torch.float32, Hq * Tq)
+    cur = _current_device()
+    b16 = torch.bfloat16
+    strides, (Tq, Tk, Hq, Hkv, D), (a, b, B) = _ragged(q, k, v, cu_q, cu_k, cur)
+    dos = _rows3(do, "do", cur, heads=Hq, D=D, dtype=b16, rows=Tq)
+    _buf(o, "o", b16, Tq * Hq * D, cur)
+    _buf(lse, "lse", torch.float32, Hq * Tq, cur)
+    dev = q.device
     if dq is None:
-        dq = torch.empty(Tq, Hq, D, dtype=torch.bfloat16, device=q.device)
+        dq = torch.empty((Tq, Hq, D), dtype=b16, device=dev)
+    else:
+        _buf(dq, "dq", b16, Tq * Hq * D, cur)
     if dk is None:
-        dk = torch.empty(Tk, Hkv, D, dtype=torch.bfloat16, device=q.device)
+        dk = torch.empty((Tk, Hkv, D), dtype=b16, device=dev)
+    else:
+        _buf(dk, "dk", b16, Tk * Hkv * D, cur)
     if dv is None:
-        dv = torch.empty(Tk, Hkv, D, dtype=torch.bfloat16, device=q.device)
-    _dev(dq, "dq", torch.bfloat16, Tq * Hq * D)
-    _dev(dk, "dk", torch.bfloat16, Tk * Hkv * D)
-    _dev(dv, "dv", torch.bfloat16, Tk * Hkv * D)
-    need = int(lib().bl_attn_backward_workspace_bytes(Tq, Tk, Hq, Hkv, D, batch[2], batch[3], batch[4], int(window),
-                                                      int(sinks)))
+        dv = torch.empty((Tk, Hkv, D), dtype=b16, device=dev)
+    else:
+        _buf(dv, "dv", b16, Tk * Hkv * D, cur)
+    L = lib()
     if workspace is None:
-        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
-    _dev(workspace, "workspace", torch.uint8)
-    rc = lib().bl_attn_backward(do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                dos, qs, ks, vs, Tq, Tk, Hq, Hkv, D, *batch, int(window), int(sinks),
-                                D ** -0.5 if scale is None else float(scale), workspace.data_ptr(), workspace.numel(),
-                                dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _stream(stream))
-    _check(rc, "bl_attn_backward")
+        need = L.bl_attn_backward_workspace_bytes(Tq, Tk, Hq, Hkv, D, B, max_q, max_k, window, sinks)
+        workspace = torch.empty(need or 16, dtype=torch.uint8, device=dev)
+    else:
+        _buf(workspace, "workspace", torch.uint8, 1, cur)
+    rc = L.bl_attn_backward(do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dos,
+                            *strides, Tq, Tk, Hq, Hkv, D, a, b, B, max_q, max_k, window, sinks,
+                            D ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.numel(),
+                            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _stream(stream))
+    if rc:
+        _check(rc, "bl_attn_backward")
     return dq, dk, dv
 
 

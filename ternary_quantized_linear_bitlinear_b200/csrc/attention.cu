@@ -144,38 +144,40 @@ inline void head_groups(int64_t group, int *parts, int *gsize) {
     *gsize = (int)((group + *parts - 1) / *parts);
 }
 
-template <bool BF16, int DP, int G, int WARPS, int OCC, int SLOTS>
+template <typename C>
 bl_status launch_decode(DecodeAttnParams &P, const AttnDevice &d, int64_t batches_at_most, cudaStream_t st) {
-    int ctas = d.sms * OCC;
+    int ctas = d.sms * C::OCC;
     if (ctas > AD_MAX_CTAS) ctas = AD_MAX_CTAS;
     // no more warps than batches
-    const int64_t need = (batches_at_most + WARPS - 1) / WARPS;
+    const int64_t need = (batches_at_most + C::WARPS - 1) / C::WARPS;
     if (need < ctas) ctas = (int)(need < 1 ? 1 : need);
-    constexpr int smem = ad_smem(WARPS, G, DP, SLOTS);
     static std::atomic<u64> ready{0};  // devices this kernel's shared memory is set up on
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return BL_ERR_CUDA;
     if (!(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
-        if (!big_smem(k_attn_decode<BF16, DP, G, WARPS, OCC, SLOTS>, smem)) return BL_ERR_CUDA;
+        if (!big_smem(k_attn_decode<C>, ad_smem<C>(C::G))) return BL_ERR_CUDA;
         ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    k_attn_decode<BF16, DP, G, WARPS, OCC, SLOTS><<<ctas, WARPS * 32, smem, st>>>(P);
+    k_attn_decode<C><<<ctas, C::WARPS * 32, ad_smem<C>(P.gsize), st>>>(P);
     if (cudaGetLastError() != cudaSuccess) return BL_ERR_CUDA;
-    return launch_after(k_attn_join<DP>, dim3((unsigned)P.B, (unsigned)(P.Hkv * P.parts)), AD_JOIN_THREADS, 0, st, P,
-                        ctas, WARPS);
+    return launch_after(k_attn_join<C::DP>, dim3((unsigned)P.B, (unsigned)P.Hq), AD_JOIN_THREADS, 0, st, P,
+                        ctas, C::WARPS);
 }
 
-template <bool BF16, int DP>
-bl_status decode_by_heads(DecodeAttnParams &P, const AttnDevice &d, int64_t batches, cudaStream_t st) {
-    // two CTAs of eight warps an SM with three slots each where registers and
-    // shared memory allow it
-    switch (P.gsize) {
-        case 1: return launch_decode<BF16, DP, 1, 8, 2, 3>(P, d, batches, st);
-        case 2: return launch_decode<BF16, DP, 2, 8, 2, 3>(P, d, batches, st);
-        case 3: return launch_decode<BF16, DP, 3, 8, 2, 3>(P, d, batches, st);
-        case 4: return launch_decode<BF16, DP, 4, 7, 2, 3>(P, d, batches, st);
-        default: return launch_decode<BF16, DP, 8, 8, 1, 4>(P, d, batches, st);
+template <int DP>
+bl_status decode_by_type(DecodeAttnParams &P, const AttnDevice &d, bool bf16_cache, int64_t batches, cudaStream_t st) {
+    if (bf16_cache) {
+        // 12 warps an SM (168 registers a thread); three slots a warp where a partial of up to 8 heads takes the
+        // room of a fourth
+        if (P.q_bf16)
+            return P.gsize <= 4 ? launch_decode<DecodeMma<DP, DEC_BF16, 4, 3, 4>>(P, d, batches, st)
+                                : launch_decode<DecodeMma<DP, DEC_BF16, 4, 3, 3>>(P, d, batches, st);
+        return P.gsize <= 4 ? launch_decode<DecodeMma<DP, DEC_F32_4, 4, 3, 4>>(P, d, batches, st)
+                            : launch_decode<DecodeMma<DP, DEC_F32_8, 4, 3, 3>>(P, d, batches, st);
     }
+    if (P.gsize == 1) return launch_decode<DecodeFma<DP, 1, 8, 2, 3>>(P, d, batches, st);
+    if (P.gsize <= 3) return launch_decode<DecodeFma<DP, 3, 8, 2, 3>>(P, d, batches, st);
+    return launch_decode<DecodeFma<DP, 8, 8, 1, 4>>(P, d, batches, st);
 }
 
 }  // namespace
@@ -276,7 +278,6 @@ bl_status bl_attn_decode(const void *q, bl_dtype xdt, int64_t q_stride, int64_t 
     P.D = (int)D;
     P.group = (int)(Hq / Hkv);
     head_groups(P.group, &P.parts, &P.gsize);
-    if (Hkv * P.parts > 65535) return BL_ERR_SHAPE;
     P.seq_ids = seq_ids;
     const int64_t most = cache->max_pages * cache->page_size;
     P.window = (int)(window > most ? most : window);
@@ -292,9 +293,8 @@ bl_status bl_attn_decode(const void *q, bl_dtype xdt, int64_t q_stride, int64_t 
     const int64_t seen = window > 0 && P.window + (int64_t)P.sinks < most ? P.window + P.sinks + 64 : most;
     const int64_t batches = B * Hkv * P.parts * (seen / 8 + 1);
     cudaStream_t st = (cudaStream_t)stream;
-    if (cache->dtype == BL_BF16)
-        return D <= 64 ? decode_by_heads<true, 64>(P, *d, batches, st) : decode_by_heads<true, 128>(P, *d, batches, st);
-    return D <= 64 ? decode_by_heads<false, 64>(P, *d, batches, st) : decode_by_heads<false, 128>(P, *d, batches, st);
+    const bool bf16 = cache->dtype == BL_BF16;
+    return D <= 64 ? decode_by_type<64>(P, *d, bf16, batches, st) : decode_by_type<128>(P, *d, bf16, batches, st);
 }
 
 // ---------------------------------------------------------------------------
