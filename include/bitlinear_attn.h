@@ -12,6 +12,7 @@
  *   - Heads: Hq query heads share Hkv key / value heads, Hq % Hkv == 0; query
  *     head h reads key head h / (Hq / Hkv).  Head size D: 16 <= D <= 128,
  *     D % 16 == 0.
+ *   - scale: positive.
  *   - Rows: q, k, v hold one row of heads per token; row t of q starts at
  *     q + t * q_stride elements (q_stride >= Hq * D, and a row must start on
  *     a 16-byte boundary), its heads are contiguous.  The q, k, v columns of

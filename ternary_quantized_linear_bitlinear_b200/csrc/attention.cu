@@ -12,6 +12,7 @@
 #include "bitlinear_attn.h"
 #include "bl_common.cuh"
 #include "k_attn_decode.cuh"
+#include "k_attn_fwd_tc.cuh"
 #include "k_attn_mma.cuh"
 #include "k_kv_pages.cuh"
 #include "k_rope_append.cuh"
@@ -60,8 +61,8 @@ bl_status attn_device(AttnDevice **out) {
         d.ok = major == 10;
         if (d.ok) {
             const int plan = (int)kv_plan_smem(KV_MAX_SEQS, KV_MAX_N, 2);
-            if (!big_smem(k_kv_extend, plan) || !big_smem(k_kv_fork_plan, plan) || !big_smem(k_attn_fwd<64>, am_smem<64>(4)) ||
-                !big_smem(k_attn_fwd<128>, am_smem<128>(4)) || !big_smem(k_attn_dq<64>, am_smem<64>(4)) ||
+            if (!big_smem(k_kv_extend, plan) || !big_smem(k_kv_fork_plan, plan) || 
+                !big_smem(k_attn_fwd_tc<64>, FwdShape<64>::SMEM) || !big_smem(k_attn_fwd_tc<128>, FwdShape<128>::SMEM) || !big_smem(k_attn_dq<64>, am_smem<64>(4)) ||
                 !big_smem(k_attn_dq<128>, am_smem<128>(4)) || !big_smem(k_attn_dkdv<64>, am_smem<64>(4)) ||
                 !big_smem(k_attn_dkdv<128>, am_smem<128>(4)))
                 return BL_ERR_CUDA;
@@ -133,6 +134,36 @@ bl_status launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t smem
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? BL_OK : BL_ERR_CUDA;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static EncodeTiled fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiled>(ptr);
+    });
+    return fn;
+}
+
+// Map of rows of heads [T, H, D] bf16 (row stride in elements): boxes of 128
+// rows x 64 columns of one head, 128-byte swizzle, zeros outside.
+bool head_map(CUtensorMap *m, const void *base, int64_t T, int64_t H, int64_t D, int64_t stride) {
+    EncodeTiled enc = encode_tiled();
+    if (enc == nullptr) return false;
+    const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+    const cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dim, str, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // ---------------------------------------------------------------------------
@@ -260,7 +291,7 @@ bl_status bl_attn_decode(const void *q, bl_dtype xdt, int64_t q_stride, int64_t 
     bl_status rc = check_heads(Hq, Hkv, D);
     if (rc) return rc;
     if (B < 1 || B > AD_MAX_B || window < 0 || sinks < 0) return BL_ERR_SHAPE;
-    if (!(scale > -1e30f && scale < 1e30f)) return BL_ERR_SHAPE;
+    if (!(scale > 0.f && scale < 1e30f)) return BL_ERR_SHAPE;
     if ((rc = check_rows(q, q_stride, Hq * D, esize(xdt)))) return rc;
     if (!aligned16(out) || !aligned4(lse) || !aligned4(seq_ids)) return BL_ERR_ALIGN;
     DecodeAttnParams P;
@@ -405,7 +436,7 @@ static bl_status ragged_params(RaggedParams *P, const void *q, const void *k, co
     if (Tq < 1 || Tk < 1 || B < 1 || B > 65535 || Tq * Hq > I32_MAX || Tk * Hkv > I32_MAX || Tq > I32_MAX || Tk > I32_MAX)
         return BL_ERR_SHAPE;
     if (max_q < 1 || max_k < 1 || max_q >= (1 << 24) || max_k >= (1 << 24) || window < 0 || sinks < 0) return BL_ERR_SHAPE;
-    if (!(scale > -1e30f && scale < 1e30f)) return BL_ERR_SHAPE;
+    if (!(scale > 0.f && scale < 1e30f)) return BL_ERR_SHAPE;
     if ((rc = check_rows(q, q_stride, Hq * D, 2)) || (rc = check_rows(k, k_stride, Hkv * D, 2)) ||
         (rc = check_rows(v, v_stride, Hkv * D, 2)))
         return rc;
@@ -450,9 +481,14 @@ bl_status bl_attn_forward(const void *q, const void *k, const void *v, int64_t q
     P.lse = lse;
     AttnDevice *d;
     if ((rc = attn_device(&d))) return rc;
-    const dim3 grid((unsigned)((P.max_q + AM_B - 1) / AM_B), (unsigned)Hq, (unsigned)B);
-    if (D <= 64) k_attn_fwd<64><<<grid, AM_T, am_smem<64>(3), (cudaStream_t)stream>>>(P);
-    else k_attn_fwd<128><<<grid, AM_T, am_smem<128>(3), (cudaStream_t)stream>>>(P);
+    RaggedMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    if (!head_map(&maps.q, q, Tq, Hq, D, q_stride) || !head_map(&maps.k, k, Tk, Hkv, D, k_stride) ||
+        !head_map(&maps.v, v, Tk, Hkv, D, v_stride))
+        return BL_ERR_CUDA;
+    const dim3 grid((unsigned)((P.max_q + AF_ROWS - 1) / AF_ROWS), (unsigned)Hq, (unsigned)B);
+    if (D <= 64) k_attn_fwd_tc<64><<<grid, AF_THREADS, FwdShape<64>::SMEM, (cudaStream_t)stream>>>(maps, P);
+    else k_attn_fwd_tc<128><<<grid, AF_THREADS, FwdShape<128>::SMEM, (cudaStream_t)stream>>>(maps, P);
     return cudaGetLastError() == cudaSuccess ? BL_OK : BL_ERR_CUDA;
 }
 

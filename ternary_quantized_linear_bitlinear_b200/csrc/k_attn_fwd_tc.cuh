@@ -1,0 +1,335 @@
+// Ragged causal attention with a sliding window and sinks, forward, on
+// tcgen05.
+//
+//   S = Q K^T, P = exp2(scale log2(e) (S - m)), O = P V / rowsum(P), one pass
+//   over the visible key tiles with the running maximum m
+//
+// A CTA owns 256 consecutive queries of one head as two halves of 128 rows
+// (TMEM lanes) that share the K and V tiles of 128 keys.  S of a half (128
+// float32 columns of TMEM) is read by its softmax warpgroup, one thread per
+// row; P goes back to TMEM as bf16 over the same columns and is the A operand
+// of O += P V, whose accumulator stays in TMEM.  While one half is in its
+// softmax the tensor core works for the other.  A half takes part only in
+// tiles that some of its rows see; a tile that all of them see whole is not
+// masked.  m moves (and O is rescaled) only when a row's maximum grows by more
+// than 2^8, which sums in float32 absorb.
+//
+// Bound by the exponentials: a 128 x 128 tile is 1024 cycles of the special
+// function unit beside 1024 cycles of tensor work at D = 128 (768 at 64).
+//
+// Warps: 0 TMA producer, 1 TMEM allocator and MMA issuer, 2 clears the rows
+// behind the last key of a partial V tile, 4 - 7 and 8 - 11 the softmax of
+// the halves.  Every wait is bounded (a wait that gives up raises the device
+// error word and the CTA's abort flag; copies and MMAs in flight are awaited,
+// bounded too, before TMEM is freed).
+#pragma once
+
+#include "k_attn_ragged.cuh"
+#include "tc05.cuh"
+
+namespace bl {
+
+constexpr int AF_THREADS = 384;
+constexpr int AF_ROWS = 256;
+constexpr int AF_KEYS = 128;
+
+template <int DP>
+struct FwdShape {
+    static constexpr int STAGES = DP == 64 ? 4 : 2;
+    static constexpr int TILE = DP / 64 * TC_BLOCK;  // 128 rows
+    static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + STAGES * TILE, OFF_BAR = OFF_V + STAGES * TILE;
+    static constexpr int BARS = 2 + 4 * STAGES + 9;
+    static constexpr int SMEM = OFF_BAR + BARS * 8 + 16 + 1024;
+};
+
+struct RaggedMaps {
+    CUtensorMap q, k, v, dout;
+};
+
+// Tiles of a CTA's halves: half h sees sink tiles below ns[h] and wt[h] .. last[h].
+struct HalfTiles {
+    int ns, wt, last;  // last < 0: none
+    __device__ __forceinline__ bool has(int t) const { return last >= 0 && (t < ns || (t >= wt && t <= last)); }
+};
+__device__ __forceinline__ HalfTiles half_tiles(const RaggedParams &p, int p0, int p1, int nk) {
+    const KeyTiles t = key_tiles<AF_KEYS>(p, p0, p1, nk);
+    HalfTiles h{t.ns, t.wt, -1};
+    if (t.count > 0) h.last = t.wt + t.count - t.ns - 1;
+    return h;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(AF_THREADS, 1)
+    k_attn_fwd_tc(const __grid_constant__ RaggedMaps maps, const __grid_constant__ RaggedParams p) {
+    using F = FwdShape<DP>;
+    constexpr int ST = F::STAGES;
+    extern __shared__ uint8_t af_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(af_raw) + 1023) & ~(uintptr_t)1023);
+    const u32 sbase = smem_u32(sm), bar0 = sbase + F::OFF_BAR;
+    const u32 QF = bar0, KF = bar0 + 16, KE = KF + 8 * ST, VF = KE + 8 * ST, VE = VF + 8 * ST, SF = VE + 8 * ST,
+              PF = SF + 16, OF = PF + 16, CUT = OF + 16, FIX = CUT + 8, DRAIN = FIX + 8;
+    u32 *s_tmem = reinterpret_cast<u32 *>(sm + F::OFF_BAR + F::BARS * 8);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(sm + F::OFF_BAR + F::BARS * 8 + 4);
+    constexpr unsigned long long TO = 2000000000ull;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.y, b = blockIdx.z;
+    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) check_entry(p, b);
+    Entry e;
+    if (!entry_of(p, b, e)) return;
+    const int i0 = (gridDim.x - 1 - blockIdx.x) * AF_ROWS;  // the longest rows first
+    if (i0 >= e.nq) return;
+    const int kvh = h / p.group;
+    const int rows0 = e.nq - i0 < 128 ? e.nq - i0 : 128;
+    const int rows1 = e.nq - i0 <= 128 ? 0 : e.nq - i0 - 128 < 128 ? e.nq - i0 - 128 : 128;
+    const int pos0 = i0 + e.off;
+    HalfTiles ht[2];
+    ht[0] = half_tiles(p, pos0, pos0 + rows0 - 1, e.nk);
+    ht[1] = HalfTiles{0, 0, -1};
+    if (rows1 > 0) ht[1] = half_tiles(p, pos0 + 128, pos0 + 128 + rows1 - 1, e.nk);
+    const KeyTiles all = key_tiles<AF_KEYS>(p, pos0, pos0 + rows0 + rows1 - 1, e.nk);
+    const int count = all.count;
+    auto tile_of = [&](int u) { return u < all.ns ? u : all.wt + (u - all.ns); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < F::BARS; ++i) mbar_init(bar0 + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(PF + 8 * i, 128);
+        *s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tc_alloc(smem_u32(s_tmem), 512);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const u32 tmem = *s_tmem;
+    // TMEM columns: S / P of the halves at 0 and 128, O at 256 and 256 + DP
+    auto s_col = [&](int half) { return tmem + 128u * half; };
+    auto o_col = [&](int half) { return tmem + 256u + (u32)DP * half; };
+    // the entry's last tile when it is partial (cut rows; then it can only be the last of this CTA): its V has a
+    // barrier of its own, and another one that says its rows behind the last key are clear
+    const int cut = e.nk % AF_KEYS;
+    const int cut_tile = cut ? e.nk / AF_KEYS : -1;
+    const bool cuts = count > 0 && tile_of(count - 1) == cut_tile;
+    auto v_full = [&](int u) { return cuts && u == count - 1 ? CUT : VF + 8 * (u % ST); };
+    auto v_phase = [&](int u) { return cuts && u == count - 1 ? 0u : (u32)((u / ST) & 1); };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool failed = false;
+            for (int half = 0; half < 2; ++half) {
+                if (ht[half].last < 0) continue;
+                mbar_arrive_expect_tx(QF + 8 * half, F::TILE);
+                tc_load_rows<DP>(&maps.q, sbase + half * F::TILE, h, e.q0 + i0 + 128 * half, QF + 8 * half);
+            }
+            int u = 0;
+            for (; u < count; ++u) {
+                const int s = u % ST, row = e.k0 + tile_of(u) * AF_KEYS;
+                const u32 ph = (u32)((u / ST) & 1) ^ 1;
+                if (u >= ST && !(mbar_wait(KE + 8 * s, ph, TO, s_abort) && mbar_wait(VE + 8 * s, ph, TO, s_abort))) {
+                    failed = true;
+                    break;
+                }
+                mbar_arrive_expect_tx(KF + 8 * s, F::TILE);
+                tc_load_rows<DP>(&maps.k, sbase + F::OFF_K + s * F::TILE, kvh, row, KF + 8 * s);
+                mbar_arrive_expect_tx(v_full(u), F::TILE);
+                tc_load_rows<DP>(&maps.v, sbase + F::OFF_V + s * F::TILE, kvh, row, v_full(u));
+            }
+            if (failed) {
+                raise_device_error(DEVERR_TIMEOUT_PRODUCER);
+                *s_abort = 1;
+            }
+            // what was requested lands before the CTA exits
+            for (int half = 0; half < 2; ++half)
+                if (ht[half].last >= 0) mbar_wait(QF + 8 * half, 0, TO, nullptr);
+            for (int j = u - ST > 0 ? u - ST : 0; j < u; ++j) {
+                mbar_wait(KF + 8 * (j % ST), (u32)((j / ST) & 1), TO, nullptr);
+                mbar_wait(v_full(j), v_phase(j), TO, nullptr);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && count > 0) {
+            constexpr u32 ID_QK = tc_idesc(AF_KEYS, false, false), ID_PV = tc_idesc(DP, false, true);
+            bool ok = true;
+            int n[2] = {0, 0};  // tiles of a half whose P was consumed
+            int k_seen = -1, v_seen = -1;
+            auto qk = [&](int half, int u) {
+                const int s = u % ST;
+                if (k_seen < u) {
+                    ok = ok && mbar_wait(KF + 8 * s, (u32)((u / ST) & 1), TO, s_abort);
+                    k_seen = u;
+                }
+                if (n[half] == 0) ok = ok && mbar_wait(QF + 8 * half, 0, TO, s_abort);
+                if (!ok) return;
+                tc_after();
+                const u32 a = sbase + half * F::TILE, k = sbase + F::OFF_K + s * F::TILE;
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; ++kk) {
+                    const u32 at = (u32)(kk / 4) * TC_BLOCK + (kk % 4) * 32;
+                    tc_mma_ss(s_col(half), tc_desc_k(a + at), tc_desc_k(k + at), ID_QK, kk != 0);
+                }
+                tc_commit(SF + 8 * half);
+            };
+            for (int half = 0; half < 2 && ok; ++half)
+                if (ht[half].has(tile_of(0))) qk(half, 0);
+            if (ok) tc_commit(KE);
+            for (int u = 0; u < count && ok; ++u) {
+                const int s = u % ST, t = tile_of(u);
+                for (int half = 0; half < 2 && ok; ++half) {
+                    if (ht[half].has(t)) {
+                        if (v_seen < u) {
+                            ok = ok && mbar_wait(t == cut_tile ? FIX : VF + 8 * s, v_phase(u), TO, s_abort);
+                            v_seen = u;
+                        }
+                        ok = ok && mbar_wait(PF + 8 * half, (u32)(n[half] & 1), TO, s_abort);
+                        if (!ok) break;
+                        tc_after();
+                        const u32 v = sbase + F::OFF_V + s * F::TILE;
+#pragma unroll
+                        for (int kk = 0; kk < AF_KEYS / 16; ++kk)
+                            tc_mma_ts(o_col(half), s_col(half) + 8 * kk, tc_desc_mn(v + kk * 2048), ID_PV,
+                                      n[half] != 0 || kk != 0);
+                        ++n[half];
+                        if (t == ht[half].last) tc_commit(OF + 8 * half);
+                    }
+                    if (u + 1 < count && ht[half].has(tile_of(u + 1))) qk(half, u + 1);
+                }
+                if (!ok) break;
+                tc_commit(VE + 8 * s);
+                if (u + 1 < count) tc_commit(KE + 8 * ((u + 1) % ST));
+            }
+            if (!ok) {
+                raise_device_error(DEVERR_TIMEOUT_MMA);
+                *s_abort = 1;
+            }
+            // everything issued completes before TMEM is freed
+            tc_commit(DRAIN);
+            mbar_wait(DRAIN, 0, TO, nullptr);
+        }
+    } else if (warp == 2) {
+        if (cuts) {
+            if (__all_sync(0xffffffffu, mbar_wait(CUT, 0, TO, s_abort))) {
+                tc_zero_rows<DP>(sm + F::OFF_V + (count - 1) % ST * F::TILE, cut);
+                if (lane == 0) mbar_arrive(FIX);
+            } else if (lane == 0) {
+                raise_device_error(DEVERR_TIMEOUT_EXPAND);
+                *s_abort = 1;
+            }
+        }
+    } else if (warp >= 4) {
+        const int half = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+        const int row = i0 + 128 * half + r, rows = half ? rows1 : rows0;
+        const int pos = row + e.off;
+        const u32 lane_at = (u32)((warp & 3) * 32) << 16;
+        const HalfTiles mine = ht[half];
+        const int first_pos = pos0 + 128 * half, last_pos = first_pos + rows - 1;
+        const float sl = p.scale_log2;
+        float m = -INFINITY, l = 0.f;
+        int n = 0;
+        bool ok = true;
+        for (int u = 0; u < count; ++u) {
+            const int t = tile_of(u);
+            if (!mine.has(t)) continue;
+            ok = __all_sync(0xffffffffu, mbar_wait(SF + 8 * half, (u32)(n & 1), TO, s_abort));
+            if (!ok) break;
+            tc_after();
+            u32 w[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc_ld32(w + 32 * c, s_col(half) + lane_at + 32 * c);
+            tc_wait_ld();
+            const int j0 = t * AF_KEYS;
+            // whole tile visible to every row of the half?
+            const bool whole = j0 + AF_KEYS - 1 <= first_pos && j0 + AF_KEYS <= e.nk &&
+                               (p.window == 0 || last_pos - j0 < p.window || j0 + AF_KEYS <= p.sinks);
+            if (!whole) {
+                const int lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 - j0 : 0;  // first key of the window
+                const int hi = (pos < e.nk - 1 ? pos : e.nk - 1) - j0;                        // last key
+                const int sk = p.sinks - j0;                                                  // keys below are sinks
+#pragma unroll
+                for (int j = 0; j < 128; ++j)
+                    if (j > hi || (j < lo && j >= sk)) w[j] = 0xff800000u;
+            }
+            float mx = __uint_as_float(w[0]);
+#pragma unroll
+            for (int j = 1; j < 128; ++j) mx = fmaxf(mx, __uint_as_float(w[j]));
+            if (__any_sync(0xffffffffu, (mx - m) * sl > 8.f || m == -INFINITY)) {
+                const float top = fmaxf(m, mx), c = m == -INFINITY ? 0.f : exp2_fast((m - top) * sl);
+                m = top;
+                l *= c;
+                if (n > 0) {
+#pragma unroll
+                    for (int k = 0; k < DP / 32; ++k) {
+                        u32 o[32];
+                        tc_ld32(o, o_col(half) + lane_at + 32 * k);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * c);
+                        tc_st32(o_col(half) + lane_at + 32 * k, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m * sl;
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                u32 pk[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float x = exp2_fast(fmaf(__uint_as_float(w[32 * c + 2 * j]), sl, -base));
+                    const float y = exp2_fast(fmaf(__uint_as_float(w[32 * c + 2 * j + 1]), sl, -base));
+                    sum0 += x;
+                    sum1 += y;
+                    pk[j] = pack_bf16(x, y);
+                }
+                tc_st16(s_col(half) + lane_at + 16 * c, pk);
+            }
+            l += sum0 + sum1;
+            tc_wait_st();
+            tc_before();
+            mbar_arrive(PF + 8 * half);
+            ++n;
+        }
+        if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(OF + 8 * half, 0, TO, s_abort));
+        if (!ok) {
+            if (lane == 0) {
+                raise_device_error(DEVERR_TIMEOUT_EPILOGUE);
+                *s_abort = 1;
+            }
+        } else if (rows > 0) {
+            tc_after();
+            const float f = l > 0.f ? 1.f / l : 0.f;
+            uint16_t *out = p.o + ((size_t)(e.q0 + row) * p.Hq + h) * p.D;
+#pragma unroll 1
+            for (int k = 0; k < DP / 32; ++k) {
+                u32 o[32];
+                if (n > 0) {
+                    tc_ld32(o, o_col(half) + lane_at + 32 * k);
+                    tc_wait_ld();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0u;
+                }
+                if (r < rows) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        if (32 * k + j < p.D)
+                            *reinterpret_cast<uint4 *>(out + 32 * k + j) =
+                                make_uint4(pack_bf16(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f),
+                                           pack_bf16(__uint_as_float(o[j + 2]) * f, __uint_as_float(o[j + 3]) * f),
+                                           pack_bf16(__uint_as_float(o[j + 4]) * f, __uint_as_float(o[j + 5]) * f),
+                                           pack_bf16(__uint_as_float(o[j + 6]) * f, __uint_as_float(o[j + 7]) * f));
+                    }
+                }
+            }
+            if (r < rows)
+                p.lse[(size_t)h * p.Tq + e.q0 + row] = l > 0.f ? m * p.scale + logf(l) : -INFINITY;
+        }
+    }
+    tc_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace bl

@@ -1,6 +1,5 @@
-// Ragged attention and its gradients on mma.sync: 64 x 64 tiles, four warps,
-// each 16 rows; operands in shared memory, one pass over the visible key
-// tiles with the running maximum and sum of the softmax.
+// Gradients of ragged attention on mma.sync: 64 x 64 tiles, four warps, each
+// 16 rows; operands in shared memory.
 #pragma once
 
 #include "k_attn_ragged.cuh"
@@ -63,81 +62,6 @@ __device__ __forceinline__ void store_rows(const float (&acc)[DP / 8][4], uint16
         if (r < rows) *reinterpret_cast<u32 *>(out + r * stride + d) = pack_bf16(acc[n][0] * f0, acc[n][1] * f0);
         if (r + 8 < rows) *reinterpret_cast<u32 *>(out + (r + 8) * stride + d) = pack_bf16(acc[n][2] * f1, acc[n][3] * f1);
     }
-}
-
-template <int DP>
-__global__ void __launch_bounds__(AM_T) k_attn_fwd(const __grid_constant__ RaggedParams p) {
-    extern __shared__ __align__(128) uint8_t sm[];
-    const u32 sq = smem_u32(sm), sk = sq + am_smem<DP>(1), sv = sk + am_smem<DP>(1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y, b = blockIdx.z;
-    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) check_entry(p, b);
-    Entry e;
-    if (!entry_of(p, b, e)) return;
-    const int i0 = (gridDim.x - 1 - blockIdx.x) * AM_B;
-    if (i0 >= e.nq) return;
-    const int rows = e.nq - i0 < AM_B ? e.nq - i0 : AM_B;
-    const int kvh = h / p.group;
-    load_tile<DP, AM_B, AM_T>(sq, p.q + (e.q0 + i0) * p.q_stride + (size_t)h * p.D, p.q_stride, rows, p.D);
-    const KeyTiles kt = key_tiles<AM_B>(p, i0 + e.off, i0 + rows - 1 + e.off, e.nk);
-    float o[DP / 8][4] = {};
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    const int row = warp * 16 + (lane >> 2);
-    const int pos[2] = {i0 + row + e.off, i0 + row + 8 + e.off};
-    for (int t = 0; t < kt.count; ++t) {
-        const int j0 = (t < kt.ns ? t : kt.wt + t - kt.ns) * AM_B;
-        const int nk = e.nk - j0 < AM_B ? e.nk - j0 : AM_B;
-        load_tile<DP, AM_B, AM_T>(sk, p.k + (e.k0 + j0) * p.k_stride + (size_t)kvh * p.D, p.k_stride, nk, p.D);
-        load_tile<DP, AM_B, AM_T>(sv, p.v + (e.k0 + j0) * p.v_stride + (size_t)kvh * p.D, p.v_stride, nk, p.D);
-        cp_commit();
-        cp_wait<0>();
-        __syncthreads();
-        float s[8][4];
-        warp_gemm_nt<DP>(s, sq, warp * 16, sk);
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int key = j0 + n * 8 + (lane & 3) * 2 + (x & 1);
-                s[n][x] = key < e.nk && sees(p, pos[x >> 1], key) ? s[n][x] * p.scale_log2 : -INFINITY;
-            }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float mx = m[r];
-#pragma unroll
-            for (int n = 0; n < 8; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * r], s[n][2 * r + 1]));
-            mx = quad_max(mx);
-            const float base = mx == -INFINITY ? 0.f : mx, c = exp2_fast(m[r] - base);
-            m[r] = mx;
-            float sum = 0.f;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                s[n][2 * r] = exp2_fast(s[n][2 * r] - base);
-                s[n][2 * r + 1] = exp2_fast(s[n][2 * r + 1] - base);
-                sum += s[n][2 * r] + s[n][2 * r + 1];
-            }
-            l[r] = l[r] * c + sum;
-#pragma unroll
-            for (int n = 0; n < DP / 8; ++n) {
-                o[n][2 * r] *= c;
-                o[n][2 * r + 1] *= c;
-            }
-        }
-        warp_gemm_nn<DP>(o, s, sv);
-        __syncthreads();
-    }
-    cp_commit();
-    cp_wait<0>();
-    float f[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const float sum = quad_sum(l[r]);
-        f[r] = sum > 0.f ? 1.f / sum : 0.f;
-        if ((lane & 3) == 0 && row + 8 * r < rows)
-            p.lse[(size_t)h * p.Tq + e.q0 + i0 + row + 8 * r] =
-                sum > 0.f ? (m[r] + log2f(sum)) * 0.693147180559945f : -INFINITY;
-    }
-    store_rows<DP>(o, p.o + ((size_t)(e.q0 + i0) * p.Hq + h) * p.D, (long long)p.Hq * p.D, rows, warp * 16, p.D, f[0], f[1]);
 }
 
 // delta[h, t] = sum_d do[t, h, d] * o[t, h, d]; one warp per row.

@@ -1,0 +1,124 @@
+// tcgen05 and TMA pieces the attention kernels share (sm_100a): descriptors
+// of 128-byte-swizzled bf16 tiles, MMA issue, TMEM loads and stores.
+//
+// A tile of R rows x 64 bf16 columns is R rows of 128 bytes in shared memory,
+// 16-byte chunks permuted by the row (SWIZZLE_128B), 1024-byte aligned; wider
+// matrices are several such blocks.  Read along its columns it is a K-major
+// operand, read along its rows (rows = the contracted index) an MN-major one.
+#pragma once
+
+#include <cuda.h>
+
+#include "bl_common.cuh"
+
+namespace bl {
+
+constexpr int TC_BLOCK = 128 * 128;  // bytes of 128 rows x 64 bf16 columns
+
+// K-major: 8-row groups 1024 bytes apart; a step of 16 columns is +32 bytes.
+__device__ __forceinline__ u64 tc_desc_k(u32 saddr) {
+    return (u64)((saddr >> 4) & 0x3FFFu) | (u64)1u << 16 | (u64)(1024u >> 4) << 32 | (u64)1u << 46 | (u64)2u << 61;
+}
+// MN-major: 64-column blocks TC_BLOCK bytes apart, 8-row groups (of the
+// contracted index) 1024 bytes apart; a step of 16 rows is +2048 bytes.
+__device__ __forceinline__ u64 tc_desc_mn(u32 saddr) {
+    return (u64)((saddr >> 4) & 0x3FFFu) | (u64)(TC_BLOCK >> 4) << 16 | (u64)(1024u >> 4) << 32 | (u64)1u << 46 |
+           (u64)2u << 61;
+}
+// D float32, A and B bf16, M = 128; transposed operands are MN-major.
+__host__ __device__ constexpr u32 tc_idesc(int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((u32)(n >> 3) << 17) |
+           ((u32)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_ss(u32 d, u64 a, u64 b, u32 idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((u32)add)
+        : "memory");
+}
+// A in TMEM (bf16 pairs, 8 columns per 16 of the contracted index).
+__device__ __forceinline__ void tc_mma_ts(u32 d, u32 a, u64 b, u32 idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((u32)add)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit(u32 bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_alloc(u32 slot, u32 cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_dealloc(u32 tmem, u32 cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this thread's TMEM lane (call tc_wait_ld before using them).
+__device__ __forceinline__ void tc_ld32(u32 *r, u32 addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st32(u32 addr, const u32 *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(u32 addr, const u32 *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+
+// 128 rows x DP columns of one head of a [T, H, D] tensor (map: D, H, T) into
+// DP / 64 blocks; rows and columns beyond the tensor are zero.
+template <int DP>
+__device__ __forceinline__ void tc_load_rows(const CUtensorMap *map, u32 dst, int head, int row, u32 bar) {
+#pragma unroll
+    for (int c = 0; c < DP; c += 64)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                dst + (u32)(c / 64) * TC_BLOCK),
+            "l"(map), "r"(c), "r"(head), "r"(row), "r"(bar)
+            : "memory");
+}
+
+// Rows from .. 127 of a tile to zero (one warp).  A tile's rows beyond its
+// sequence belong to others or to nobody: their values must not meet a zero
+// weight in a product, which would make NaN of an infinity.
+template <int DP>
+__device__ __forceinline__ void tc_zero_rows(uint8_t *tile, int from) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c)
+        for (int i = from * 8 + lane; i < 128 * 8; i += 32)
+            reinterpret_cast<uint4 *>(tile + c * TC_BLOCK)[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
+}  // namespace bl
