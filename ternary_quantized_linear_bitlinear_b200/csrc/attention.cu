@@ -11,9 +11,9 @@
 
 #include "bitlinear_attn.h"
 #include "bl_common.cuh"
+#include "k_attn_bwd_tc.cuh"
 #include "k_attn_decode.cuh"
 #include "k_attn_fwd_tc.cuh"
-#include "k_attn_mma.cuh"
 #include "k_kv_pages.cuh"
 #include "k_rope_append.cuh"
 
@@ -61,10 +61,10 @@ bl_status attn_device(AttnDevice **out) {
         d.ok = major == 10;
         if (d.ok) {
             const int plan = (int)kv_plan_smem(KV_MAX_SEQS, KV_MAX_N, 2);
-            if (!big_smem(k_kv_extend, plan) || !big_smem(k_kv_fork_plan, plan) || 
-                !big_smem(k_attn_fwd_tc<64>, FwdShape<64>::SMEM) || !big_smem(k_attn_fwd_tc<128>, FwdShape<128>::SMEM) || !big_smem(k_attn_dq<64>, am_smem<64>(4)) ||
-                !big_smem(k_attn_dq<128>, am_smem<128>(4)) || !big_smem(k_attn_dkdv<64>, am_smem<64>(4)) ||
-                !big_smem(k_attn_dkdv<128>, am_smem<128>(4)))
+            if (!big_smem(k_kv_extend, plan) || !big_smem(k_kv_fork_plan, plan) ||
+                !big_smem(k_attn_fwd_tc<64>, FwdShape<64>::SMEM) || !big_smem(k_attn_fwd_tc<128>, FwdShape<128>::SMEM) ||
+                !big_smem(k_attn_dq_tc<64>, DqShape<64>::SMEM) || !big_smem(k_attn_dq_tc<128>, DqShape<128>::SMEM) ||
+                !big_smem(k_attn_dkdv_tc<64>, DkvShape<64>::SMEM) || !big_smem(k_attn_dkdv_tc<128>, DkvShape<128>::SMEM))
                 return BL_ERR_CUDA;
         }
         d.init = true;
@@ -494,9 +494,10 @@ bl_status bl_attn_forward(const void *q, const void *k, const void *v, int64_t q
 
 size_t bl_attn_backward_workspace_bytes(int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, int64_t B,
                                         int64_t max_q, int64_t max_k, int64_t window, int64_t sinks) {
-    (void)B, (void)max_q, (void)max_k, (void)window, (void)sinks;
-    if (Tq < 1 || Tk < 1 || check_heads(Hq, Hkv, D) != BL_OK) return 0;
-    return align256((size_t)Tq * Hq * 4);
+    if (Tq < 1 || Tk < 1 || B < 1 || max_q < 1 || max_k < 1 || window < 0 || sinks < 0 || check_heads(Hq, Hkv, D) != BL_OK)
+        return 0;
+    const DkvCut cut = dkv_cut(max_q, max_k, window, sinks);
+    return align256((size_t)Tq * Hq * 4) + sink_slot(cut, (int)Hkv, (int)D, (int)B, 0, 0, 0) * 4;
 }
 
 bl_status bl_attn_backward(const void *do_, const void *q, const void *k, const void *v, const void *o,
@@ -527,16 +528,25 @@ bl_status bl_attn_backward(const void *do_, const void *q, const void *k, const 
     AttnDevice *d;
     if ((rc = attn_device(&d))) return rc;
     cudaStream_t st = (cudaStream_t)stream;
-    k_attn_delta<<<(unsigned)((Tq * Hq + 7) / 8), 256, 0, st>>>(P, delta);
-    const dim3 gq((unsigned)((P.max_q + AM_B - 1) / AM_B), (unsigned)Hq, (unsigned)B);
-    const dim3 gk((unsigned)((P.max_k + AM_B - 1) / AM_B), (unsigned)Hkv, (unsigned)B);
+    RaggedMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    if (!head_map(&maps.q, q, Tq, Hq, D, q_stride) || !head_map(&maps.k, k, Tk, Hkv, D, k_stride) ||
+        !head_map(&maps.v, v, Tk, Hkv, D, v_stride) || !head_map(&maps.dout, do_, Tq, Hq, D, do_stride))
+        return BL_ERR_CUDA;
+    const DkvCut cut = dkv_cut(P.max_q, P.max_k, P.window, P.sinks);
+    float *sums = delta + align256((size_t)Tq * Hq * 4) / 4;
+    const dim3 gq((unsigned)((P.max_q + 127) / 128), (unsigned)Hq, (unsigned)B);
+    const dim3 gk((unsigned)(cut.tiles + cut.sink_tiles * cut.pieces), (unsigned)Hkv, (unsigned)B);
+    // dQ first: it leaves delta for dK
     if (D <= 64) {
-        k_attn_dkdv<64><<<gk, AM_T, am_smem<64>(4), st>>>(P);
-        k_attn_dq<64><<<gq, AM_T, am_smem<64>(4), st>>>(P);
+        k_attn_dq_tc<64><<<gq, AB_THREADS, DqShape<64>::SMEM, st>>>(maps, P, delta);
+        k_attn_dkdv_tc<64><<<gk, AB_THREADS, DkvShape<64>::SMEM, st>>>(maps, P, cut, sums);
     } else {
-        k_attn_dkdv<128><<<gk, AM_T, am_smem<128>(4), st>>>(P);
-        k_attn_dq<128><<<gq, AM_T, am_smem<128>(4), st>>>(P);
+        k_attn_dq_tc<128><<<gq, AB_THREADS, DqShape<128>::SMEM, st>>>(maps, P, delta);
+        k_attn_dkdv_tc<128><<<gk, AB_THREADS, DkvShape<128>::SMEM, st>>>(maps, P, cut, sums);
     }
+    if (cut.sink_tiles > 0)
+        k_attn_sink_sum<<<dim3((unsigned)cut.sink_tiles, (unsigned)Hkv, (unsigned)B), 256, 0, st>>>(P, cut, sums);
     return cudaGetLastError() == cudaSuccess ? BL_OK : BL_ERR_CUDA;
 }
 

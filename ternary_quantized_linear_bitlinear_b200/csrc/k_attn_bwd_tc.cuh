@@ -1,0 +1,709 @@
+// Gradients of ragged causal attention with a sliding window and sinks, on
+// tcgen05, without atomics: one kernel forms dQ row tile by row tile, another
+// dK and dV key tile by key tile; both rebuild P = exp2(scale log2(e) S -
+// lse) from the scores.
+//
+//   dP = dO V^T,  dS = P o (dP - delta),  dQ = scale dS K
+//   dV = P^T dO,  dK = scale dS^T Q
+//
+// k_attn_dq_tc.  A CTA owns 128 queries of one head (TMEM lanes).  S and dP of
+// a key tile come from two products; dS goes back to TMEM as bf16 over S and
+// is the A operand of dQ += dS K.  S is double buffered: while the softmax
+// threads turn S(j), dP(j) into dS(j) the tensor core forms dQ(j - 1), dP(j)
+// and S(j + 1).  delta = rowsum(dO o O) starts the kernel; on the way it sums
+// P dP, the same quantity without O's bf16 rounding, which dK uses.
+//
+// k_attn_dkdv_tc.  A CTA owns 128 keys of one kv head (TMEM lanes) and walks
+// the query tiles that see them, for every query head that shares them, so dK
+// and dV of shared heads are sums in TMEM.  The scores are formed transposed
+// (S^T = K Q^T, dP^T = V dO^T): P^T and dS^T then lie with the keys in the
+// lanes, as the A operands of dV += P^T dO and dK += dS^T Q need them, and no
+// tile is ever transposed through shared memory.  The tensor core works one
+// step behind the threads: dV(j), S(j + 1) while they form dS(j), dK(j),
+// dP(j + 1) while they form P(j + 1).
+// A tile with sinks is seen by every later query of its sequence.  Its rows
+// beyond the window's reach are cut into pieces of their own, whose float32
+// sums go to the workspace and are added in order by k_attn_sink_sum.
+//
+// Bound: seven products of 512 tensor cycles per pair of 128-tiles at D = 128
+// against 2 x 1024 cycles of exponentials.
+//
+// Threads: warp 0 TMA producer, 1 TMEM allocator and MMA issuer, 2 rows'
+// statistics and the clearing of rows that belong to nobody, 4 - 11 the
+// softmax (two threads per lane, half of the columns each).  Waits are
+// bounded as in the forward kernel.
+#pragma once
+
+#include "k_attn_fwd_tc.cuh"
+
+namespace bl {
+
+constexpr int AB_THREADS = 384;
+constexpr unsigned long long AB_TIMEOUT_NS = 2000000000ull;
+
+// ---------------------------------------------------------------------------
+// dQ
+
+template <int DP>
+struct DqShape {
+    static constexpr int KS = 3, VS = 2;  // stages of K (read twice, two steps apart) and V
+    static constexpr int TILE = DP / 64 * TC_BLOCK;
+    static constexpr int OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE, OFF_D = OFF_V + VS * TILE;
+    static constexpr int OFF_BAR = OFF_D + 2 * 128 * 4;
+    static constexpr int BARS = 1 + 2 * KS + 2 * VS + 8;
+    static constexpr int SMEM = OFF_BAR + BARS * 8 + 16 + 1024;
+};
+static_assert(DqShape<128>::SMEM <= 227 * 1024, "dQ shared memory");
+
+template <int DP>
+__global__ void __launch_bounds__(AB_THREADS, 1)
+    k_attn_dq_tc(const __grid_constant__ RaggedMaps maps, const __grid_constant__ RaggedParams p, float *delta_out) {
+    using F = DqShape<DP>;
+    constexpr int KS = F::KS, VS = F::VS;
+    extern __shared__ uint8_t af_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(af_raw) + 1023) & ~(uintptr_t)1023);
+    const u32 sbase = smem_u32(sm), bar0 = sbase + F::OFF_BAR;
+    const u32 QF = bar0, KF = bar0 + 8, KE = KF + 8 * KS, VF = KE + 8 * KS, VE = VF + 8 * VS, SF = VE + 8 * VS,
+              DPF = SF + 16, DSR = DPF + 8, OUT = DSR + 8, CUT = OUT + 8, FIX = CUT + 8, DRAIN = FIX + 8;
+    float *s_delta = reinterpret_cast<float *>(sm + F::OFF_D);  // [2][128]
+    u32 *s_tmem = reinterpret_cast<u32 *>(sm + F::OFF_BAR + F::BARS * 8);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(sm + F::OFF_BAR + F::BARS * 8 + 4);
+    constexpr unsigned long long TO = AB_TIMEOUT_NS;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.y, b = blockIdx.z;
+    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) check_entry(p, b);
+    Entry e;
+    if (!entry_of(p, b, e)) return;
+    const int i0 = (gridDim.x - 1 - blockIdx.x) * 128;
+    if (i0 >= e.nq) return;
+    const int kvh = h / p.group;
+    const int rows = e.nq - i0 < 128 ? e.nq - i0 : 128;
+    const int first_pos = i0 + e.off, last_pos = first_pos + rows - 1;
+    const KeyTiles all = key_tiles<AF_KEYS>(p, first_pos, last_pos, e.nk);
+    const int n = all.count;
+    auto tile_of = [&](int u) { return u < all.ns ? u : all.wt + (u - all.ns); };
+    // the entry's last tile when it is partial: K and V on a barrier of their own, then cleared behind the last key
+    const int cut = e.nk % AF_KEYS;
+    const bool cuts = n > 0 && cut != 0 && tile_of(n - 1) == e.nk / AF_KEYS;
+    auto k_full = [&](int u) { return cuts && u == n - 1 ? FIX : KF + 8 * (u % KS); };
+    auto v_full = [&](int u) { return cuts && u == n - 1 ? FIX : VF + 8 * (u % VS); };
+    auto k_phase = [&](int u) { return cuts && u == n - 1 ? 0u : (u32)((u / KS) & 1); };
+    auto v_phase = [&](int u) { return cuts && u == n - 1 ? 0u : (u32)((u / VS) & 1); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < F::BARS; ++i) mbar_init(bar0 + 8 * i, 1);
+        mbar_init(DSR, 256);
+        *s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tc_alloc(smem_u32(s_tmem), 512);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const u32 tmem = *s_tmem;
+    auto s_col = [&](int j) { return tmem + 128u * (j & 1); };
+    const u32 dp_col = tmem + 256, dq_col = tmem + 384;
+
+    if (warp == 0) {
+        if (lane == 0 && n > 0) {
+            bool ok = true;
+            mbar_arrive_expect_tx(QF, 2 * F::TILE);
+            tc_load_rows<DP>(&maps.q, sbase, h, e.q0 + i0, QF);
+            tc_load_rows<DP>(&maps.dout, sbase + F::OFF_DO, h, e.q0 + i0, QF);
+            int u = 0;
+            for (; u < n; ++u) {
+                const int ks = u % KS, vs = u % VS, row = e.k0 + tile_of(u) * AF_KEYS;
+                if (u >= KS) ok = ok && mbar_wait(KE + 8 * ks, (u32)((u / KS) & 1) ^ 1, TO, s_abort);
+                if (u >= VS) ok = ok && mbar_wait(VE + 8 * vs, (u32)((u / VS) & 1) ^ 1, TO, s_abort);
+                if (!ok) break;
+                if (cuts && u == n - 1) {
+                    mbar_arrive_expect_tx(CUT, 2 * F::TILE);
+                    tc_load_rows<DP>(&maps.k, sbase + F::OFF_K + ks * F::TILE, kvh, row, CUT);
+                    tc_load_rows<DP>(&maps.v, sbase + F::OFF_V + vs * F::TILE, kvh, row, CUT);
+                } else {
+                    mbar_arrive_expect_tx(KF + 8 * ks, F::TILE);
+                    tc_load_rows<DP>(&maps.k, sbase + F::OFF_K + ks * F::TILE, kvh, row, KF + 8 * ks);
+                    mbar_arrive_expect_tx(VF + 8 * vs, F::TILE);
+                    tc_load_rows<DP>(&maps.v, sbase + F::OFF_V + vs * F::TILE, kvh, row, VF + 8 * vs);
+                }
+            }
+            if (!ok) {
+                raise_device_error(DEVERR_TIMEOUT_PRODUCER);
+                *s_abort = 1;
+            }
+            // what was requested lands before the CTA exits
+            mbar_wait(QF, 0, TO, nullptr);
+            for (int j = u - KS > 0 ? u - KS : 0; j < u; ++j) {
+                if (cuts && j == n - 1) {
+                    mbar_wait(CUT, 0, TO, nullptr);
+                } else {
+                    mbar_wait(KF + 8 * (j % KS), (u32)((j / KS) & 1), TO, nullptr);
+                    if (j >= u - VS) mbar_wait(VF + 8 * (j % VS), (u32)((j / VS) & 1), TO, nullptr);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && n > 0) {
+            constexpr u32 ID_S = tc_idesc(AF_KEYS, false, false), ID_Q = tc_idesc(DP, false, true);
+            bool ok = mbar_wait(QF, 0, TO, s_abort);
+            auto form = [&](u32 d, u32 a, u32 bt) {
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; ++kk) {
+                    const u32 at = (u32)(kk / 4) * TC_BLOCK + (kk % 4) * 32;
+                    tc_mma_ss(d, tc_desc_k(a + at), tc_desc_k(bt + at), ID_S, kk != 0);
+                }
+            };
+            auto form_s = [&](int u) {
+                ok = ok && mbar_wait(k_full(u), k_phase(u), TO, s_abort);
+                if (!ok) return;
+                tc_after();
+                form(s_col(u), sbase, sbase + F::OFF_K + u % KS * F::TILE);
+                tc_commit(SF + 8 * (u & 1));
+            };
+            auto form_dp = [&](int u) {
+                ok = ok && mbar_wait(v_full(u), v_phase(u), TO, s_abort);
+                if (!ok) return;
+                tc_after();
+                form(dp_col, sbase + F::OFF_DO, sbase + F::OFF_V + u % VS * F::TILE);
+                tc_commit(DPF);
+                tc_commit(VE + 8 * (u % VS));
+            };
+            if (ok) form_s(0);
+            if (ok) form_dp(0);
+            if (ok && n > 1) form_s(1);
+            for (int u = 0; u < n && ok; ++u) {
+                ok = ok && mbar_wait(DSR, (u32)(u & 1), TO, s_abort);
+                if (!ok) break;
+                tc_after();
+                const u32 k = sbase + F::OFF_K + u % KS * F::TILE;
+                // columns 0 - 63 of dS are at the buffer's start, 64 - 127 at its column 64
+#pragma unroll
+                for (int kk = 0; kk < AF_KEYS / 16; ++kk)
+                    tc_mma_ts(dq_col, s_col(u) + (kk / 4) * 64 + (kk % 4) * 8, tc_desc_mn(k + kk * 2048), ID_Q,
+                              u != 0 || kk != 0);
+                tc_commit(KE + 8 * (u % KS));
+                if (u + 1 < n) form_dp(u + 1);
+                if (ok && u + 2 < n) form_s(u + 2);
+            }
+            if (ok) tc_commit(OUT);
+            else {
+                raise_device_error(DEVERR_TIMEOUT_MMA);
+                *s_abort = 1;
+            }
+            tc_commit(DRAIN);
+            mbar_wait(DRAIN, 0, TO, nullptr);
+        }
+    } else if (warp == 2) {
+        if (cuts) {
+            if (__all_sync(0xffffffffu, mbar_wait(CUT, 0, TO, s_abort))) {
+                tc_zero_rows<DP>(sm + F::OFF_K + (n - 1) % KS * F::TILE, cut);
+                tc_zero_rows<DP>(sm + F::OFF_V + (n - 1) % VS * F::TILE, cut);
+                if (lane == 0) mbar_arrive(FIX);
+            } else if (lane == 0) {
+                raise_device_error(DEVERR_TIMEOUT_EXPAND);
+                *s_abort = 1;
+            }
+        }
+    } else if (warp >= 4) {
+        const int c = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;  // columns 64 c .. 64 c + 63 of row r
+        const int row = i0 + r, pos = r < rows ? row + e.off : -1;
+        const u32 lane_at = (u32)((warp & 3) * 32) << 16;
+        const float sl = p.scale_log2;
+        const size_t stat = (size_t)h * p.Tq + e.q0 + row;
+        // delta: this thread's half of the row's columns
+        float part = 0.f;
+        if (r < rows) {
+            const uint16_t *od = p.dout + (e.q0 + row) * p.do_stride + (size_t)h * p.D;
+            const uint16_t *oo = p.o + ((size_t)(e.q0 + row) * p.Hq + h) * p.D;
+            for (int d = c * 8; d < p.D; d += 16) {
+                float x[8], y[8];
+                load8<true>(reinterpret_cast<const uint8_t *>(od + d), x);
+                load8<true>(reinterpret_cast<const uint8_t *>(oo + d), y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) part += x[i] * y[i];
+            }
+        }
+        s_delta[c * 128 + r] = part;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        float delta = s_delta[r] + s_delta[128 + r];
+        // (a row that sees nothing has lse = -inf and only hidden keys)
+        const float lse = r < rows ? p.lse[stat] * 1.44269504088896f : 0.f;
+        float sum = 0.f;
+        bool ok = true;
+        for (int u = 0; u < n; ++u) {
+            ok = __all_sync(0xffffffffu, mbar_wait(SF + 8 * (u & 1), (u32)((u >> 1) & 1), TO, s_abort));
+            if (!ok && n > 1) break;
+            tc_after();
+            u32 w[64];
+            tc_ld32(w, s_col(u) + lane_at + 64 * c);
+            tc_ld32(w + 32, s_col(u) + lane_at + 64 * c + 32);
+            tc_wait_ld();
+            const int j0 = tile_of(u) * AF_KEYS;
+            const bool whole = j0 + AF_KEYS - 1 <= first_pos && j0 + AF_KEYS <= e.nk && rows == 128 &&
+                               (p.window == 0 || last_pos - j0 < p.window || j0 + AF_KEYS <= p.sinks);
+#pragma unroll
+            for (int j = 0; j < 64; ++j) w[j] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(w[j]), sl, -lse)));
+            if (!whole) {
+                const int at = j0 + 64 * c;
+                const int lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 - at : 0;
+                const int hi = (pos < e.nk - 1 ? pos : e.nk - 1) - at;
+                const int sk = p.sinks - at;
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    if (j > hi || (j < lo && j >= sk)) w[j] = 0u;
+            }
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(DPF, (u32)(u & 1), TO, s_abort));
+            if (n == 1) {
+                // one tile holds all the row sees: delta without O's rounding, which weighs most on rows of few
+                // keys (the two halves of the columns meet at the barrier whatever the waits said)
+                tc_after();
+                part = 0.f;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    u32 g[32];
+                    tc_ld32(g, dp_col + lane_at + 64 * c + 32 * q);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) part = fmaf(__uint_as_float(w[32 * q + j]), __uint_as_float(g[j]), part);
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                s_delta[c * 128 + r] = part;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                delta = s_delta[r] + s_delta[128 + r];
+            }
+            if (!ok) break;
+            tc_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                u32 g[32], pk[16];
+                tc_ld32(g, dp_col + lane_at + 64 * c + 32 * q);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float p0 = __uint_as_float(w[32 * q + 2 * j]), p1 = __uint_as_float(w[32 * q + 2 * j + 1]);
+                    const float d0 = __uint_as_float(g[2 * j]), d1 = __uint_as_float(g[2 * j + 1]);
+                    sum = fmaf(p0, d0, fmaf(p1, d1, sum));
+                    pk[j] = pack_bf16(p0 * (d0 - delta), p1 * (d1 - delta));
+                }
+                tc_st16(s_col(u) + lane_at + 64 * c + 16 * q, pk);
+            }
+            tc_wait_st();
+            tc_before();
+            mbar_arrive(DSR);
+        }
+        if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(OUT, 0, TO, s_abort));
+        if (!ok) {
+            if (lane == 0) {
+                raise_device_error(DEVERR_TIMEOUT_EPILOGUE);
+                *s_abort = 1;
+            }
+        } else {
+            tc_after();
+            uint16_t *out = p.dq + ((size_t)(e.q0 + row) * p.Hq + h) * p.D;
+#pragma unroll 1
+            for (int k = c * DP / 64; k < (c + 1) * DP / 64; ++k) {
+                u32 o[32];
+                if (n > 0) {
+                    tc_ld32(o, dq_col + lane_at + 32 * k);
+                    tc_wait_ld();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0u;
+                }
+                if (r < rows) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8)
+                        if (32 * k + j < p.D) {
+                            const float f = p.scale;
+                            *reinterpret_cast<uint4 *>(out + 32 * k + j) =
+                                make_uint4(pack_bf16(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f),
+                                           pack_bf16(__uint_as_float(o[j + 2]) * f, __uint_as_float(o[j + 3]) * f),
+                                           pack_bf16(__uint_as_float(o[j + 4]) * f, __uint_as_float(o[j + 5]) * f),
+                                           pack_bf16(__uint_as_float(o[j + 6]) * f, __uint_as_float(o[j + 7]) * f));
+                        }
+                }
+            }
+        }
+        // the row's sum of P dP over both halves of the columns (the barriers are met whatever the waits said)
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        s_delta[c * 128 + r] = sum;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (ok && c == 0 && r < rows) delta_out[stat] = s_delta[r] + s_delta[128 + r];
+    }
+    tc_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dK, dV
+
+template <int DP>
+struct DkvShape {
+    static constexpr int ST = 2;
+    static constexpr int TILE = DP / 64 * TC_BLOCK;
+    static constexpr int OFF_V = TILE, OFF_Q = 2 * TILE, OFF_DO = OFF_Q + ST * TILE, OFF_L = OFF_DO + ST * TILE;
+    static constexpr int OFF_BAR = OFF_L + ST * 2 * 128 * 4;
+    static constexpr int BARS = 1 + 3 * ST + 6;
+    static constexpr int SMEM = OFF_BAR + BARS * 8 + 16 + 1024;
+};
+static_assert(DkvShape<128>::SMEM <= 227 * 1024, "dK, dV shared memory");
+
+// How a launch is cut: `tiles` key tiles of every entry, the first
+// `sink_tiles` of them with `pieces` more CTAs each for the queries beyond the
+// window's reach, `chunk` query tiles (of every head) per piece.
+struct DkvCut {
+    int tiles, sink_tiles, pieces, chunk;
+};
+
+inline DkvCut dkv_cut(int64_t max_q, int64_t max_k, int64_t window, int64_t sinks) {
+    DkvCut c{(int)((max_k + 127) / 128), 0, 0, 0};
+    if (window > 0 && sinks > 0) {
+        const int64_t qt = (max_q + 127) / 128 + 1;
+        // as many query tiles as an ordinary key tile has
+        c.chunk = (int)((window + 127) / 128 + 1 < 4 ? 4 : (window + 127) / 128 + 1);
+        if (qt > c.chunk) {
+            const int64_t st = ((sinks < max_k ? sinks : max_k) + 127) / 128;
+            c.sink_tiles = (int)st;
+            c.pieces = (int)((qt + c.chunk - 1) / c.chunk);
+        }
+    }
+    return c;
+}
+
+// float32 sums of sink tile t of (b, kvh): [piece 0 .. pieces][dk, dv][128][D]
+__host__ __device__ inline size_t sink_slot(const DkvCut &c, int Hkv, int D, int b, int kvh, int t, int piece) {
+    return (((((size_t)b * Hkv + kvh) * c.sink_tiles + t) * (c.pieces + 1) + piece) * 2) * 128 * D;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(AB_THREADS, 1)
+    k_attn_dkdv_tc(const __grid_constant__ RaggedMaps maps, const __grid_constant__ RaggedParams p,
+                   const __grid_constant__ DkvCut cutting, float *sums) {
+    using F = DkvShape<DP>;
+    constexpr int ST = F::ST;
+    extern __shared__ uint8_t af_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(af_raw) + 1023) & ~(uintptr_t)1023);
+    const u32 sbase = smem_u32(sm), bar0 = sbase + F::OFF_BAR;
+    const u32 KVF = bar0, QF = bar0 + 8, QE = QF + 8 * ST, LF = QE + 8 * ST, SF = LF + 8 * ST, DPF = SF + 8, PR = DPF + 8,
+              DSR = PR + 8, OUT = DSR + 8, DRAIN = OUT + 8;
+    float *s_stat = reinterpret_cast<float *>(sm + F::OFF_L);  // [stage][lse, delta][128]
+    u32 *s_tmem = reinterpret_cast<u32 *>(sm + F::OFF_BAR + F::BARS * 8);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(sm + F::OFF_BAR + F::BARS * 8 + 4);
+    constexpr unsigned long long TO = AB_TIMEOUT_NS;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kvh = blockIdx.y, b = blockIdx.z;
+    Entry e;
+    if (!entry_of(p, b, e)) return;
+    // the sink tiles' pieces come first, then the key tiles
+    const int extra = cutting.sink_tiles * cutting.pieces;
+    const bool far = (int)blockIdx.x < extra;
+    const int t = far ? (int)blockIdx.x / cutting.pieces : (int)blockIdx.x - extra;
+    const int piece = far ? (int)blockIdx.x % cutting.pieces + 1 : 0;
+    const int j0 = t * 128;
+    if (j0 >= e.nk) return;
+    const int keys = e.nk - j0 < 128 ? e.nk - j0 : 128;
+    // query tiles that see the tile: from its first key's query on, to the window's reach of its last key
+    int q_lo = j0 - e.off, q_hi = e.nq - 1;
+    if (q_lo < 0) q_lo = 0;
+    int t_lo = q_lo / 128, t_hi = q_hi >= q_lo ? q_hi / 128 : t_lo - 1;  // tiles t_lo .. t_hi
+    const bool sink = j0 < p.sinks && p.window > 0;
+    if (sink && t < cutting.sink_tiles) {
+        // the main CTA keeps the first `chunk` tiles, piece i the i-th `chunk` after them
+        t_lo += piece * cutting.chunk;
+        if (t_hi > t_lo + cutting.chunk - 1) t_hi = t_lo + cutting.chunk - 1;
+    } else if (p.window > 0 && !sink) {
+        const long long last = (long long)j0 + keys - 1 + p.window - 1 - e.off;
+        if (last < q_hi) t_hi = last < q_lo ? t_lo - 1 : (int)(last / 128);
+    }
+    const bool to_sums = t < cutting.sink_tiles;
+    const int qt = t_hi - t_lo + 1 > 0 ? t_hi - t_lo + 1 : 0, n = qt * p.group;
+    if (far && n == 0) return;  // (its sums are not read)
+    auto head_of = [&](int u) { return kvh * p.group + u / qt; };
+    auto row_of = [&](int u) { return (t_lo + u % qt) * 128; };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < F::BARS; ++i) mbar_init(bar0 + 8 * i, 1);
+        mbar_init(PR, 256);
+        mbar_init(DSR, 256);
+        *s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tc_alloc(smem_u32(s_tmem), 512);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const u32 tmem = *s_tmem;
+    const u32 s_col = tmem, dp_col = tmem + 128, dv_col = tmem + 256, dk_col = tmem + 384;
+
+    if (warp == 0) {
+        if (lane == 0 && n > 0) {
+            bool ok = true;
+            mbar_arrive_expect_tx(KVF, 2 * F::TILE);
+            tc_load_rows<DP>(&maps.k, sbase, kvh, e.k0 + j0, KVF);
+            tc_load_rows<DP>(&maps.v, sbase + F::OFF_V, kvh, e.k0 + j0, KVF);
+            int u = 0;
+            for (; u < n; ++u) {
+                const int s = u % ST, row = e.q0 + row_of(u), h = head_of(u);
+                if (u >= ST && !mbar_wait(QE + 8 * s, (u32)((u / ST) & 1) ^ 1, TO, s_abort)) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(QF + 8 * s, 2 * F::TILE);
+                tc_load_rows<DP>(&maps.q, sbase + F::OFF_Q + s * F::TILE, h, row, QF + 8 * s);
+                tc_load_rows<DP>(&maps.dout, sbase + F::OFF_DO + s * F::TILE, h, row, QF + 8 * s);
+            }
+            if (!ok) {
+                raise_device_error(DEVERR_TIMEOUT_PRODUCER);
+                *s_abort = 1;
+            }
+            mbar_wait(KVF, 0, TO, nullptr);
+            for (int j = u - ST > 0 ? u - ST : 0; j < u; ++j) mbar_wait(QF + 8 * (j % ST), (u32)((j / ST) & 1), TO, nullptr);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && n > 0) {
+            constexpr u32 ID_S = tc_idesc(128, false, false), ID_O = tc_idesc(DP, false, true);
+            bool ok = mbar_wait(KVF, 0, TO, s_abort);
+            auto form = [&](u32 d, u32 a, u32 bt) {
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; ++kk) {
+                    const u32 at = (u32)(kk / 4) * TC_BLOCK + (kk % 4) * 32;
+                    tc_mma_ss(d, tc_desc_k(a + at), tc_desc_k(bt + at), ID_S, kk != 0);
+                }
+            };
+            // columns 0 - 63 of P, dS are at the region's start, 64 - 127 at its column 64
+            auto add = [&](u32 d, u32 a, u32 bt, bool more) {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc_mma_ts(d, a + (kk / 4) * 64 + (kk % 4) * 8, tc_desc_mn(bt + kk * 2048), ID_O, more || kk != 0);
+            };
+            auto q_at = [&](int u) { return sbase + F::OFF_Q + u % ST * F::TILE; };
+            auto do_at = [&](int u) { return sbase + F::OFF_DO + u % ST * F::TILE; };
+            auto q_ready = [&](int u) {
+                const u32 ph = (u32)((u / ST) & 1);
+                ok = ok && mbar_wait(QF + 8 * (u % ST), ph, TO, s_abort) && mbar_wait(LF + 8 * (u % ST), ph, TO, s_abort);
+                tc_after();
+            };
+            q_ready(0);
+            if (ok) {
+                form(s_col, sbase, q_at(0));
+                tc_commit(SF);
+                form(dp_col, sbase + F::OFF_V, do_at(0));
+                tc_commit(DPF);
+            }
+            for (int u = 0; u < n && ok; ++u) {
+                ok = mbar_wait(PR, (u32)(u & 1), TO, s_abort);
+                if (!ok) break;
+                tc_after();
+                add(dv_col, s_col, do_at(u), u != 0);
+                if (u + 1 < n) {
+                    q_ready(u + 1);
+                    if (!ok) break;
+                    form(s_col, sbase, q_at(u + 1));
+                    tc_commit(SF);
+                }
+                ok = mbar_wait(DSR, (u32)(u & 1), TO, s_abort);
+                if (!ok) break;
+                tc_after();
+                add(dk_col, dp_col, q_at(u), u != 0);
+                tc_commit(QE + 8 * (u % ST));
+                if (u + 1 < n) {
+                    form(dp_col, sbase + F::OFF_V, do_at(u + 1));
+                    tc_commit(DPF);
+                }
+            }
+            if (ok) tc_commit(OUT);
+            else {
+                raise_device_error(DEVERR_TIMEOUT_MMA);
+                *s_abort = 1;
+            }
+            tc_commit(DRAIN);
+            mbar_wait(DRAIN, 0, TO, nullptr);
+        }
+    } else if (warp == 2) {
+        // lse and delta of a query tile; rows behind the last query are cleared and get weights of zero
+        bool ok = true;
+        for (int u = 0; u < n; ++u) {
+            const int s = u % ST, i0 = row_of(u);
+            const int rows = e.nq - i0 < 128 ? e.nq - i0 : 128;
+            float lse[4], delta[4];
+            const size_t stat = (size_t)head_of(u) * p.Tq + e.q0 + i0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = lane + 32 * k;
+                lse[k] = r < rows ? p.lse[stat + r] : -INFINITY;
+                delta[k] = r < rows ? p.delta[stat + r] : 0.f;
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(QF + 8 * s, (u32)((u / ST) & 1), TO, s_abort));
+            if (!ok) break;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // a query that sees nothing has lse = -inf: its weights are exp2(S - inf) = 0 as well
+                s_stat[(s * 2) * 128 + lane + 32 * k] = lse[k] == -INFINITY ? INFINITY : lse[k] * 1.44269504088896f;
+                s_stat[(s * 2 + 1) * 128 + lane + 32 * k] = delta[k];
+            }
+            if (rows < 128) {
+                tc_zero_rows<DP>(sm + F::OFF_Q + s * F::TILE, rows);
+                tc_zero_rows<DP>(sm + F::OFF_DO + s * F::TILE, rows);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(LF + 8 * s);
+        }
+        if (!ok && lane == 0) {
+            raise_device_error(DEVERR_TIMEOUT_EXPAND);
+            *s_abort = 1;
+        }
+    } else if (warp >= 4) {
+        const int c = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;  // columns (queries) 64 c .. + 63 of key r
+        const int key = j0 + r;
+        const u32 lane_at = (u32)((warp & 3) * 32) << 16;
+        const float sl = p.scale_log2;
+        bool ok = true;
+        for (int u = 0; u < n; ++u) {
+            const int s = u % ST, i0 = row_of(u);
+            ok = __all_sync(0xffffffffu, mbar_wait(LF + 8 * s, (u32)((u / ST) & 1), TO, s_abort) &&
+                                             mbar_wait(SF, (u32)(u & 1), TO, s_abort));
+            if (!ok) break;
+            tc_after();
+            u32 w[64];
+            tc_ld32(w, s_col + lane_at + 64 * c);
+            tc_ld32(w + 32, s_col + lane_at + 64 * c + 32);
+            const float4 *lse = reinterpret_cast<const float4 *>(s_stat + (s * 2) * 128 + 64 * c);
+            const float4 *del = reinterpret_cast<const float4 *>(s_stat + (s * 2 + 1) * 128 + 64 * c);
+            tc_wait_ld();
+            const int first = i0 + e.off;  // position of column 0
+            const bool whole = j0 + 127 <= first && (p.window == 0 || first + 127 - j0 < p.window || j0 + 128 <= p.sinks);
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) {
+                const float4 x = lse[j / 4];
+                w[j] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(w[j]), sl, -x.x)));
+                w[j + 1] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(w[j + 1]), sl, -x.y)));
+                w[j + 2] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(w[j + 2]), sl, -x.z)));
+                w[j + 3] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(w[j + 3]), sl, -x.w)));
+            }
+            if (!whole) {
+                const int lo = key - first - 64 * c;                                                 // first query
+                const int hi = p.window > 0 && key >= p.sinks ? lo + p.window : 0x7fffffff;  // behind the last one
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    if (j < lo || j >= hi) w[j] = 0u;
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                u32 pk[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    pk[j] = pack_bf16(__uint_as_float(w[32 * q + 2 * j]), __uint_as_float(w[32 * q + 2 * j + 1]));
+                tc_st16(s_col + lane_at + 64 * c + 16 * q, pk);
+            }
+            tc_wait_st();
+            tc_before();
+            mbar_arrive(PR);
+            ok = __all_sync(0xffffffffu, mbar_wait(DPF, (u32)(u & 1), TO, s_abort));
+            if (!ok) break;
+            tc_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                u32 g[32], pk[16];
+                tc_ld32(g, dp_col + lane_at + 64 * c + 32 * q);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    const float4 x = del[8 * q + j / 2];
+                    pk[j] = pack_bf16(__uint_as_float(w[32 * q + 2 * j]) * (__uint_as_float(g[2 * j]) - x.x),
+                                      __uint_as_float(w[32 * q + 2 * j + 1]) * (__uint_as_float(g[2 * j + 1]) - x.y));
+                    pk[j + 1] = pack_bf16(__uint_as_float(w[32 * q + 2 * j + 2]) * (__uint_as_float(g[2 * j + 2]) - x.z),
+                                          __uint_as_float(w[32 * q + 2 * j + 3]) * (__uint_as_float(g[2 * j + 3]) - x.w));
+                }
+                tc_st16(dp_col + lane_at + 64 * c + 16 * q, pk);
+            }
+            tc_wait_st();
+            tc_before();
+            mbar_arrive(DSR);
+        }
+        if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(OUT, 0, TO, s_abort));
+        if (!ok) {
+            if (lane == 0) {
+                raise_device_error(DEVERR_TIMEOUT_EPILOGUE);
+                *s_abort = 1;
+            }
+        } else {
+            tc_after();
+            // the first four warps write dV, the others dK
+            const float f = c == 0 ? 1.f : p.scale;
+            uint16_t *out = (c == 0 ? p.dv : p.dk) + ((size_t)(e.k0 + key) * p.Hkv + kvh) * p.D;
+            float *acc = nullptr;
+            if (to_sums)
+                acc = sums + sink_slot(cutting, p.Hkv, p.D, b, kvh, t, piece) + ((size_t)(c == 0 ? 1 : 0) * 128 + r) * p.D;
+#pragma unroll 1
+            for (int k = 0; k < DP / 32; ++k) {
+                u32 o[32];
+                if (n > 0) {
+                    tc_ld32(o, (c == 0 ? dv_col : dk_col) + lane_at + 32 * k);
+                    tc_wait_ld();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0u;
+                }
+                if (r < keys) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        if (32 * k + j >= p.D) continue;
+                        float x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[j + i]) * f;
+                        if (to_sums) store8(reinterpret_cast<uint8_t *>(acc + 32 * k + j), x, false);
+                        else store8(reinterpret_cast<uint8_t *>(out + 32 * k + j), x, true);
+                    }
+                }
+            }
+        }
+    }
+    tc_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+// Sink tiles: the pieces' float32 sums, in order, to dk and dv.  One CTA per
+// (sink tile, kv head, entry).
+__global__ void __launch_bounds__(256) k_attn_sink_sum(const __grid_constant__ RaggedParams p,
+                                                       const __grid_constant__ DkvCut cutting, const float *sums) {
+    const int t = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+    Entry e;
+    if (!entry_of(p, b, e)) return;
+    const int j0 = t * 128;
+    if (j0 >= e.nk) return;
+    const int keys = e.nk - j0 < 128 ? e.nk - j0 : 128;
+    const int q_lo = j0 - e.off > 0 ? j0 - e.off : 0;
+    const int t_lo = q_lo / 128, t_hi = e.nq - 1 >= q_lo ? (e.nq - 1) / 128 : t_lo - 1;
+    // pieces that had query tiles (piece 0, the main CTA, always wrote)
+    const int tiles = t_hi - t_lo + 1;
+    int pieces = (tiles + cutting.chunk - 1) / cutting.chunk;
+    if (pieces > cutting.pieces + 1) pieces = cutting.pieces + 1;
+    if (pieces < 1) pieces = 1;
+    const float *base = sums + sink_slot(cutting, p.Hkv, p.D, b, kvh, t, 0);
+    const size_t step = (size_t)2 * 128 * p.D;
+    for (int i = threadIdx.x * 8; i < 2 * keys * p.D; i += 256 * 8) {
+        const int which = i / (keys * p.D), at = i - which * keys * p.D;  // 0: dk, 1: dv
+        const int r = at / p.D, d = at - r * p.D;
+        float x[8] = {};
+        for (int k = 0; k < pieces; ++k) {
+            float y[8];
+            load8<false>(reinterpret_cast<const uint8_t *>(base + k * step + ((size_t)which * 128 + r) * p.D + d), y);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) x[c] += y[c];
+        }
+        uint16_t *out = (which == 0 ? p.dk : p.dv) + ((size_t)(e.k0 + j0 + r) * p.Hkv + kvh) * p.D + d;
+        store8(reinterpret_cast<uint8_t *>(out), x, true);
+    }
+}
+
+}  // namespace bl
