@@ -114,7 +114,10 @@ bl_status bl_attn_decode(const void *q, bl_dtype xdt, int64_t q_stride, int64_t 
 /* n <= 8192.                                                                */
 /*                                                                           */
 /* bl_kv_extend  entry i's sequence grows by counts[i] tokens: pages for     */
-/*               them, lengths += counts                                     */
+/*               them, lengths += counts; active [n] int32 (or NULL) = the   */
+/*               ids, or -1 for each when the call failed: used as the       */
+/*               seq_ids of bl_rope_append and bl_attn_decode it keeps a     */
+/*               step that got no pages from writing anything                */
 /* bl_kv_free    the sequences end: each of their pages' refs -= 1, table    */
 /*               rows -1, lengths 0; an id listed twice, or of an empty      */
 /*               sequence, does nothing more; ids >= max_seqs are skipped    */
@@ -132,7 +135,7 @@ bl_status bl_attn_decode(const void *q, bl_dtype xdt, int64_t q_stride, int64_t 
 /* ------------------------------------------------------------------------ */
 bl_status bl_kv_extend(int32_t *tables, int32_t *lengths, int32_t *refs, int64_t num_pages, int64_t page_size,
                        int64_t max_seqs, int64_t max_pages, const int32_t *seq_ids, const int32_t *counts,
-                       int64_t n, int32_t *status, bl_stream_t stream);
+                       int64_t n, int32_t *status, int32_t *active, bl_stream_t stream);
 bl_status bl_kv_free(int32_t *tables, int32_t *lengths, int32_t *refs, int64_t num_pages, int64_t page_size,
                      int64_t max_seqs, int64_t max_pages, const int32_t *seq_ids, int64_t n, bl_stream_t stream);
 size_t bl_kv_fork_workspace_bytes(int64_t n);

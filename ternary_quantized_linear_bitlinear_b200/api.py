@@ -108,7 +108,7 @@ _SIGS = {
     "bl_attn_decode_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
     "bl_attn_decode": (_int, [_p, _int, _i64, _i64, _i64, _i64, _i64, _p, _p, _i64, _i64, _f32, _p,
                               _sz, _p, _p, _p]),
-    "bl_kv_extend": (_int, [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _p]),
+    "bl_kv_extend": (_int, [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _p, _p]),
     "bl_kv_free": (_int, [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _i64, _p]),
     "bl_kv_fork_workspace_bytes": (_sz, [_i64]),
     "bl_kv_fork": (_int, [_p, _i64, _i64, _p, _p, _p, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _sz, _p, _p]),
@@ -734,7 +734,8 @@ def bl_rope_append(q=None, k=None, v=None, rope=None, cu_seqlens=None, lengths=N
         _i32(seq_ids, "seq_ids", B, cur)
     if rope is not None and not (_ok(rope, torch.float32, cur) and rope.dim() == 2 and rope.shape[1] == D):
         _dev(rope, "rope", torch.float32)
-        raise ValueError(f"rope must be [positions, {D}]")
+        if rope.dim() != 2 or rope.shape[1] != D:
+            raise ValueError(f"rope must be [positions, {D}]")
     cache = None
     max_seqs = 0
     if (k_pages is None) != (v_pages is None):
@@ -824,18 +825,21 @@ def _status(status, like, cur: int):
     return status
 
 
-def bl_kv_extend(tables, lengths, refs, seq_ids, counts, page_size: int, status=None, stream=None):
+def bl_kv_extend(tables, lengths, refs, seq_ids, counts, page_size: int, status=None, active=None, stream=None):
     """Sequence seq_ids[i] grows by counts[i] tokens: pages from the lowest free
     ones, lengths raised -> status int32 [1] (0: done; otherwise nothing was
-    changed, see bitlinear_attn.h)."""
+    changed, see bitlinear_attn.h).  active int32 [n], when given, becomes
+    seq_ids, or -1 throughout when the call failed."""
     cur = _current_device()
     max_seqs, max_pages = _tables2(tables, lengths, refs, cur)
     ids = _buf(seq_ids, "seq_ids", torch.int32, 1, cur)
     n = seq_ids.numel()
     cnt = _i32(counts, "counts", n, cur)
     status = _status(status, tables, cur)
+    if active is not None:
+        _i32(active, "active", n, cur)
     rc = lib().bl_kv_extend(tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(), refs.numel(), page_size, max_seqs,
-                            max_pages, ids, cnt, n, status.data_ptr(), _stream(stream))
+                            max_pages, ids, cnt, n, status.data_ptr(), _ptr(active), _stream(stream))
     if rc:
         _check(rc, "bl_kv_extend")
     return status

@@ -333,18 +333,18 @@ bl_status bl_attn_decode(const void *q, bl_dtype xdt, int64_t q_stride, int64_t 
 
 bl_status bl_kv_extend(int32_t *tables, int32_t *lengths, int32_t *refs, int64_t num_pages, int64_t page_size,
                        int64_t max_seqs, int64_t max_pages, const int32_t *seq_ids, const int32_t *counts,
-                       int64_t n, int32_t *status, bl_stream_t stream) {
+                       int64_t n, int32_t *status, int32_t *active, bl_stream_t stream) {
     if (!tables || !lengths || !refs || !seq_ids || !counts || !status) return BL_ERR_NULL;
     bl_status rc = check_tables(num_pages, page_size, max_seqs, max_pages);
     if (rc) return rc;
     if (n < 1 || n > KV_MAX_N) return BL_ERR_SHAPE;
     if (!aligned4(tables) || !aligned4(lengths) || !aligned4(refs) || !aligned4(seq_ids) || !aligned4(counts) ||
-        !aligned4(status))
+        !aligned4(status) || !aligned4(active))
         return BL_ERR_ALIGN;
     AttnDevice *d;
     if ((rc = attn_device(&d))) return rc;
     const KvExtendParams P{{tables, lengths, refs, (int)num_pages, (int)max_seqs, (int)max_pages, log2_of(page_size)},
-                           seq_ids, counts, (int)n, status};
+                           seq_ids, counts, (int)n, status, active};
     k_kv_extend<<<1, KV_THREADS, kv_plan_smem((int)max_seqs, (int)n, 1), (cudaStream_t)stream>>>(P);
     return cudaGetLastError() == cudaSuccess ? BL_OK : BL_ERR_CUDA;
 }

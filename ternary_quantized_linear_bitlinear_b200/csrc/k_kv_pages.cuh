@@ -90,6 +90,7 @@ struct KvExtendParams {
     const int *ids, *counts;
     int n;
     int *status;
+    int *active;  // [n] or NULL: the ids when the call succeeds, else -1
 };
 
 __global__ void __launch_bounds__(KV_THREADS) k_kv_extend(const __grid_constant__ KvExtendParams p) {
@@ -133,6 +134,8 @@ __global__ void __launch_bounds__(KV_THREADS) k_kv_extend(const __grid_constant_
     const long long free_pages = count_free(p.t.refs, p.t.num_pages, scratch);
     const int status = *bad ? *bad : sum > free_pages ? KV_NO_PAGES : KV_OK;
     if (threadIdx.x == 0) *p.status = status;
+    if (p.active != nullptr)
+        for (int i = threadIdx.x; i < p.n; i += KV_THREADS) p.active[i] = status == KV_OK ? p.ids[i] : -1;
     if (status != KV_OK) return;
     const int want = (int)sum;
     if (threadIdx.x == 0) first[p.n] = want;
