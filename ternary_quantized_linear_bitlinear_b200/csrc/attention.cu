@@ -48,6 +48,15 @@ bool big_smem(K kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
 
+// Whether a kernel's registers at launch cover what its warpgroups ask for
+// later (a request beyond them would wait for ever).
+template <typename K>
+bool covers_split(K kernel) {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kernel) == cudaSuccess &&
+           a.numRegs * AF_THREADS >= 128 * (AF_REGS_LOW + 2 * AF_REGS_HIGH);
+}
+
 bl_status attn_device(AttnDevice **out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return BL_ERR_CUDA;
@@ -61,6 +70,7 @@ bl_status attn_device(AttnDevice **out) {
         d.ok = major == 10;
         if (d.ok) {
             const int plan = (int)kv_plan_smem(KV_MAX_SEQS, KV_MAX_N, 2);
+            if (!covers_split(k_attn_fwd_tc<64>) || !covers_split(k_attn_fwd_tc<128>)) return BL_ERR_CUDA;
             if (!big_smem(k_kv_extend, plan) || !big_smem(k_kv_fork_plan, plan) ||
                 !big_smem(k_attn_fwd_tc<64>, FwdShape<64>::SMEM) || !big_smem(k_attn_fwd_tc<128>, FwdShape<128>::SMEM) ||
                 !big_smem(k_attn_dq_tc<64>, DqShape<64>::SMEM) || !big_smem(k_attn_dq_tc<128>, DqShape<128>::SMEM) ||

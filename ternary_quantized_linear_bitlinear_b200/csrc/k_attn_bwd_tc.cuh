@@ -50,7 +50,7 @@ struct DqShape {
     static constexpr int TILE = DP / 64 * TC_BLOCK;
     static constexpr int OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE, OFF_D = OFF_V + VS * TILE;
     static constexpr int OFF_BAR = OFF_D + 2 * 128 * 4;
-    static constexpr int BARS = 1 + 2 * KS + 2 * VS + 8;
+    static constexpr int BARS = 1 + 2 * KS + 2 * VS + 9;
     static constexpr int SMEM = OFF_BAR + BARS * 8 + 16 + 1024;
 };
 static_assert(DqShape<128>::SMEM <= 227 * 1024, "dQ shared memory");
@@ -64,13 +64,13 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(af_raw) + 1023) & ~(uintptr_t)1023);
     const u32 sbase = smem_u32(sm), bar0 = sbase + F::OFF_BAR;
     const u32 QF = bar0, KF = bar0 + 8, KE = KF + 8 * KS, VF = KE + 8 * KS, VE = VF + 8 * VS, SF = VE + 8 * VS,
-              DPF = SF + 16, DSR = DPF + 8, OUT = DSR + 8, CUT = OUT + 8, FIX = CUT + 8, DRAIN = FIX + 8;
+              DPF = SF + 16, DSR = DPF + 8, OUT = DSR + 16, CUT = OUT + 8, FIX = CUT + 8, DRAIN = FIX + 8;
     float *s_delta = reinterpret_cast<float *>(sm + F::OFF_D);  // [2][128]
     u32 *s_tmem = reinterpret_cast<u32 *>(sm + F::OFF_BAR + F::BARS * 8);
     volatile int *s_abort = reinterpret_cast<volatile int *>(sm + F::OFF_BAR + F::BARS * 8 + 4);
     constexpr unsigned long long TO = AB_TIMEOUT_NS;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int h = blockIdx.y, b = blockIdx.z;
     if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) check_entry(p, b);
     Entry e;
@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::BARS; ++i) mbar_init(bar0 + 8 * i, 1);
         mbar_init(DSR, 256);
+        mbar_init(DSR + 8, 256);
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     tc_before();
     __syncthreads();
     tc_after();
-    const u32 tmem = *s_tmem;
+    const u32 tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
     auto s_col = [&](int j) { return tmem + 128u * (j & 1); };
     const u32 dp_col = tmem + 256, dq_col = tmem + 384;
 
@@ -114,8 +115,8 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             int u = 0;
             for (; u < n; ++u) {
                 const int ks = u % KS, vs = u % VS, row = e.k0 + tile_of(u) * AF_KEYS;
-                if (u >= KS) ok = ok && mbar_wait(KE + 8 * ks, (u32)((u / KS) & 1) ^ 1, TO, s_abort);
-                if (u >= VS) ok = ok && mbar_wait(VE + 8 * vs, (u32)((u / VS) & 1) ^ 1, TO, s_abort);
+                if (u >= KS) ok = ok && tc_wait(KE + 8 * ks, (u32)((u / KS) & 1) ^ 1, TO, s_abort);
+                if (u >= VS) ok = ok && tc_wait(VE + 8 * vs, (u32)((u / VS) & 1) ^ 1, TO, s_abort);
                 if (!ok) break;
                 if (cuts && u == n - 1) {
                     mbar_arrive_expect_tx(CUT, 2 * F::TILE);
@@ -133,70 +134,90 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 *s_abort = 1;
             }
             // what was requested lands before the CTA exits
-            mbar_wait(QF, 0, TO, nullptr);
+            tc_wait(QF, 0, TO, nullptr);
             for (int j = u - KS > 0 ? u - KS : 0; j < u; ++j) {
                 if (cuts && j == n - 1) {
-                    mbar_wait(CUT, 0, TO, nullptr);
+                    tc_wait(CUT, 0, TO, nullptr);
                 } else {
-                    mbar_wait(KF + 8 * (j % KS), (u32)((j / KS) & 1), TO, nullptr);
-                    if (j >= u - VS) mbar_wait(VF + 8 * (j % VS), (u32)((j / VS) & 1), TO, nullptr);
+                    tc_wait(KF + 8 * (j % KS), (u32)((j / KS) & 1), TO, nullptr);
+                    if (j >= u - VS) tc_wait(VF + 8 * (j % VS), (u32)((j / VS) & 1), TO, nullptr);
                 }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             constexpr u32 ID_S = tc_idesc(AF_KEYS, false, false), ID_Q = tc_idesc(DP, false, true);
-            bool ok = mbar_wait(QF, 0, TO, s_abort);
-            auto form = [&](u32 d, u32 a, u32 bt) {
-#pragma unroll
-                for (int kk = 0; kk < DP / 16; ++kk) {
-                    const u32 at = (u32)(kk / 4) * TC_BLOCK + (kk % 4) * 32;
-                    tc_mma_ss(d, tc_desc_k(a + at), tc_desc_k(bt + at), ID_S, kk != 0);
-                }
-            };
+            const bool leader = tc_elect();
+            bool ok = TC_WAIT_ALL(QF, 0, TO, s_abort);
+            const u64 q_desc = tc_desc_k(sbase), do_desc = tc_desc_k(sbase + F::OFF_DO), k_desc = tc_desc_k(sbase + F::OFF_K),
+                      v_desc = tc_desc_k(sbase + F::OFF_V), kt_desc = tc_desc_mn(sbase + F::OFF_K);
             auto form_s = [&](int u) {
-                ok = ok && mbar_wait(k_full(u), k_phase(u), TO, s_abort);
+                ok = ok && TC_WAIT_ALL(k_full(u), k_phase(u), TO, s_abort);
                 if (!ok) return;
                 tc_after();
-                form(s_col(u), sbase, sbase + F::OFF_K + u % KS * F::TILE);
-                tc_commit(SF + 8 * (u & 1));
+                if (leader) {
+                    tc_gemm_nt<DP>(s_col(u), q_desc, k_desc + (u64)(u % KS * F::TILE >> 4), ID_S);
+                    tc_commit(SF + 8 * (u & 1));
+                }
+                __syncwarp();
             };
             auto form_dp = [&](int u) {
-                ok = ok && mbar_wait(v_full(u), v_phase(u), TO, s_abort);
+                ok = ok && TC_WAIT_ALL(v_full(u), v_phase(u), TO, s_abort);
                 if (!ok) return;
                 tc_after();
-                form(dp_col, sbase + F::OFF_DO, sbase + F::OFF_V + u % VS * F::TILE);
-                tc_commit(DPF);
-                tc_commit(VE + 8 * (u % VS));
+                if (leader) {
+                    tc_gemm_nt<DP>(dp_col, do_desc, v_desc + (u64)(u % VS * F::TILE >> 4), ID_S);
+                    tc_commit(DPF);
+                    tc_commit(VE + 8 * (u % VS));
+                }
+                __syncwarp();
             };
-            if (ok) form_s(0);
-            if (ok) form_dp(0);
-            if (ok && n > 1) form_s(1);
+            form_s(0);
+            form_dp(0);
+            if (n > 1) form_s(1);
             for (int u = 0; u < n && ok; ++u) {
-                ok = ok && mbar_wait(DSR, (u32)(u & 1), TO, s_abort);
+                const u64 k = kt_desc + (u64)(u % KS * F::TILE >> 4);
+                // columns 0 - 63 of dS are at the buffer's start, 64 - 127 at its column 64; the first half of each is
+                // ready first (part 0: steps 0, 1, 4, 5)
+                auto add = [&](int part) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int kk = (i & 1) + (i >> 1) * 4 + 2 * part;
+                        tc_mma_ts(dq_col, s_col(u) + (kk / 4) * 64 + (kk % 4) * 8, k + (u64)(kk * 2048 >> 4), ID_Q,
+                                  u != 0 || part != 0 || i != 0);
+                    }
+                };
+                ok = TC_WAIT_ALL(DSR, (u32)(u & 1), TO, s_abort);
                 if (!ok) break;
                 tc_after();
-                const u32 k = sbase + F::OFF_K + u % KS * F::TILE;
-                // columns 0 - 63 of dS are at the buffer's start, 64 - 127 at its column 64
-#pragma unroll
-                for (int kk = 0; kk < AF_KEYS / 16; ++kk)
-                    tc_mma_ts(dq_col, s_col(u) + (kk / 4) * 64 + (kk % 4) * 8, tc_desc_mn(k + kk * 2048), ID_Q,
-                              u != 0 || kk != 0);
-                tc_commit(KE + 8 * (u % KS));
+                if (leader) add(0);
+                __syncwarp();
+                ok = TC_WAIT_ALL(DSR + 8, (u32)(u & 1), TO, s_abort);
+                if (!ok) break;
+                tc_after();
+                // dP first: the threads wait for it next
                 if (u + 1 < n) form_dp(u + 1);
-                if (ok && u + 2 < n) form_s(u + 2);
+                if (leader) {
+                    add(1);
+                    tc_commit(KE + 8 * (u % KS));
+                }
+                __syncwarp();
+                if (u + 2 < n) form_s(u + 2);
             }
-            if (ok) tc_commit(OUT);
-            else {
+            if (!ok && lane == 0) {
                 raise_device_error(DEVERR_TIMEOUT_MMA);
                 *s_abort = 1;
             }
-            tc_commit(DRAIN);
-            mbar_wait(DRAIN, 0, TO, nullptr);
+            if (leader) {
+                if (ok) tc_commit(OUT);
+                tc_commit(DRAIN);
+            }
+            __syncwarp();
+            tc_wait(DRAIN, 0, TO, nullptr);
         }
     } else if (warp == 2) {
         if (cuts) {
-            if (__all_sync(0xffffffffu, mbar_wait(CUT, 0, TO, s_abort))) {
+            if (__all_sync(0xffffffffu, tc_wait(CUT, 0, TO, s_abort))) {
                 tc_zero_rows<DP>(sm + F::OFF_K + (n - 1) % KS * F::TILE, cut);
                 tc_zero_rows<DP>(sm + F::OFF_V + (n - 1) % VS * F::TILE, cut);
                 if (lane == 0) mbar_arrive(FIX);
@@ -211,28 +232,44 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
         const u32 lane_at = (u32)((warp & 3) * 32) << 16;
         const float sl = p.scale_log2;
         const size_t stat = (size_t)h * p.Tq + e.q0 + row;
-        // delta: this thread's half of the row's columns
-        float part = 0.f;
-        if (r < rows) {
-            const uint16_t *od = p.dout + (e.q0 + row) * p.do_stride + (size_t)h * p.D;
-            const uint16_t *oo = p.o + ((size_t)(e.q0 + row) * p.Hq + h) * p.D;
-            for (int d = c * 8; d < p.D; d += 16) {
-                float x[8], y[8];
-                load8<true>(reinterpret_cast<const uint8_t *>(od + d), x);
-                load8<true>(reinterpret_cast<const uint8_t *>(oo + d), y);
+        // delta: each warp takes 16 rows, 16 lanes a row (one row per thread instead, its loads a row apart, took 12 000
+        // of the kernel's 58 000 cycles)
+        {
+            const int w8 = warp - 4, sub = lane & 15;
+            uint4 x[8], y[8];
+            const bool in_d = sub * 8 < p.D;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) part += x[i] * y[i];
+            for (int k = 0; k < 8; ++k) {
+                // (a row or column that is not there reads the tile's first element instead: no branch between loads)
+                const int rr = w8 * 16 + 2 * k + (lane >> 4);
+                const size_t t = (size_t)(e.q0 + i0 + (rr < rows ? rr : 0));
+                const int d = in_d ? sub * 8 : 0;
+                x[k] = *reinterpret_cast<const uint4 *>(p.dout + t * p.do_stride + (size_t)h * p.D + d);
+                y[k] = *reinterpret_cast<const uint4 *>(p.o + (t * p.Hq + h) * p.D + d);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const u32 a[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, c4[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+                float part = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    part += __uint_as_float(a[i] << 16) * __uint_as_float(c4[i] << 16) +
+                            __uint_as_float(a[i] & 0xffff0000u) * __uint_as_float(c4[i] & 0xffff0000u);
+                if (!in_d) part = 0.f;
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+                if (sub == 0) s_delta[w8 * 16 + 2 * k + (lane >> 4)] = part;
             }
         }
-        s_delta[c * 128 + r] = part;
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        float delta = s_delta[r] + s_delta[128 + r];
+        float delta = s_delta[r];
         // (a row that sees nothing has lse = -inf and only hidden keys)
         const float lse = r < rows ? p.lse[stat] * 1.44269504088896f : 0.f;
-        float sum = 0.f;
+        const f32x2 sl2 = pack2(sl, sl), nlse2 = pack2(-lse, -lse);
+        f32x2 sum2 = 0ull;
         bool ok = true;
         for (int u = 0; u < n; ++u) {
-            ok = __all_sync(0xffffffffu, mbar_wait(SF + 8 * (u & 1), (u32)((u >> 1) & 1), TO, s_abort));
+            ok = __all_sync(0xffffffffu, tc_wait(SF + 8 * (u & 1), (u32)((u >> 1) & 1), TO, s_abort));
             if (!ok && n > 1) break;
             tc_after();
             u32 w[64];
@@ -243,7 +280,12 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             const bool whole = j0 + AF_KEYS - 1 <= first_pos && j0 + AF_KEYS <= e.nk && rows == 128 &&
                                (p.window == 0 || last_pos - j0 < p.window || j0 + AF_KEYS <= p.sinks);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) w[j] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(w[j]), sl, -lse)));
+            for (int j = 0; j < 64; j += 2) {
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])), sl2, nlse2), x, y);
+                w[j] = __float_as_uint(exp2_fast(x));
+                w[j + 1] = __float_as_uint(exp2_fast(y));
+            }
             if (!whole) {
                 const int at = j0 + 64 * c;
                 const int lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 - at : 0;
@@ -253,12 +295,12 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 for (int j = 0; j < 64; ++j)
                     if (j > hi || (j < lo && j >= sk)) w[j] = 0u;
             }
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(DPF, (u32)(u & 1), TO, s_abort));
+            ok = ok && __all_sync(0xffffffffu, tc_wait(DPF, (u32)(u & 1), TO, s_abort));
             if (n == 1) {
                 // one tile holds all the row sees: delta without O's rounding, which weighs most on rows of few
                 // keys (the two halves of the columns meet at the barrier whatever the waits said)
                 tc_after();
-                part = 0.f;
+                float part = 0.f;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     u32 g[32];
@@ -274,6 +316,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             }
             if (!ok) break;
             tc_after();
+            const f32x2 nd2 = pack2(-delta, -delta);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 u32 g[32], pk[16];
@@ -281,18 +324,20 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 tc_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const float p0 = __uint_as_float(w[32 * q + 2 * j]), p1 = __uint_as_float(w[32 * q + 2 * j + 1]);
-                    const float d0 = __uint_as_float(g[2 * j]), d1 = __uint_as_float(g[2 * j + 1]);
-                    sum = fmaf(p0, d0, fmaf(p1, d1, sum));
-                    pk[j] = pack_bf16(p0 * (d0 - delta), p1 * (d1 - delta));
+                    const f32x2 pp = pack2(__uint_as_float(w[32 * q + 2 * j]), __uint_as_float(w[32 * q + 2 * j + 1]));
+                    const f32x2 dd = pack2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
+                    sum2 = fma2(pp, dd, sum2);
+                    float x, y;
+                    unpack2(mul2(pp, add2(dd, nd2)), x, y);
+                    pk[j] = pack_bf16(x, y);
                 }
                 tc_st16(s_col(u) + lane_at + 64 * c + 16 * q, pk);
+                tc_wait_st();
+                tc_before();
+                mbar_arrive(DSR + 8 * q);
             }
-            tc_wait_st();
-            tc_before();
-            mbar_arrive(DSR);
         }
-        if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(OUT, 0, TO, s_abort));
+        if (ok && n > 0) ok = __all_sync(0xffffffffu, tc_wait(OUT, 0, TO, s_abort));
         if (!ok) {
             if (lane == 0) {
                 raise_device_error(DEVERR_TIMEOUT_EPILOGUE);
@@ -300,34 +345,17 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             }
         } else {
             tc_after();
-            uint16_t *out = p.dq + ((size_t)(e.q0 + row) * p.Hq + h) * p.D;
-#pragma unroll 1
-            for (int k = c * DP / 64; k < (c + 1) * DP / 64; ++k) {
-                u32 o[32];
-                if (n > 0) {
-                    tc_ld32(o, dq_col + lane_at + 32 * k);
-                    tc_wait_ld();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0u;
-                }
-                if (r < rows) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8)
-                        if (32 * k + j < p.D) {
-                            const float f = p.scale;
-                            *reinterpret_cast<uint4 *>(out + 32 * k + j) =
-                                make_uint4(pack_bf16(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f),
-                                           pack_bf16(__uint_as_float(o[j + 2]) * f, __uint_as_float(o[j + 3]) * f),
-                                           pack_bf16(__uint_as_float(o[j + 4]) * f, __uint_as_float(o[j + 5]) * f),
-                                           pack_bf16(__uint_as_float(o[j + 6]) * f, __uint_as_float(o[j + 7]) * f));
-                        }
-                }
-            }
+            // (the Q tile is not read any more)
+            const int first = 32 * (warp & 3);
+            tc_store_rows<DP / 2>(dq_col + lane_at + DP / 2 * c, n == 0, p.scale, sm + (warp - 4) * 32 * DP,
+                                  p.dq + ((size_t)(e.q0 + i0 + first) * p.Hq + h) * p.D + DP / 2 * c,
+                                  (long long)p.Hq * p.D, rows - first, p.D - DP / 2 * c);
         }
         // the row's sum of P dP over both halves of the columns (the barriers are met whatever the waits said)
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        s_delta[c * 128 + r] = sum;
+        float sum, sum_hi;
+        unpack2(sum2, sum, sum_hi);
+        s_delta[c * 128 + r] = sum + sum_hi;
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (ok && c == 0 && r < rows) delta_out[stat] = s_delta[r] + s_delta[128 + r];
     }
@@ -348,7 +376,7 @@ struct DkvShape {
     static constexpr int TILE = DP / 64 * TC_BLOCK;
     static constexpr int OFF_V = TILE, OFF_Q = 2 * TILE, OFF_DO = OFF_Q + ST * TILE, OFF_L = OFF_DO + ST * TILE;
     static constexpr int OFF_BAR = OFF_L + ST * 2 * 128 * 4;
-    static constexpr int BARS = 1 + 3 * ST + 6;
+    static constexpr int BARS = 1 + 3 * ST + 8;
     static constexpr int SMEM = OFF_BAR + BARS * 8 + 16 + 1024;
 };
 static_assert(DkvShape<128>::SMEM <= 227 * 1024, "dK, dV shared memory");
@@ -390,13 +418,13 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(af_raw) + 1023) & ~(uintptr_t)1023);
     const u32 sbase = smem_u32(sm), bar0 = sbase + F::OFF_BAR;
     const u32 KVF = bar0, QF = bar0 + 8, QE = QF + 8 * ST, LF = QE + 8 * ST, SF = LF + 8 * ST, DPF = SF + 8, PR = DPF + 8,
-              DSR = PR + 8, OUT = DSR + 8, DRAIN = OUT + 8;
-    float *s_stat = reinterpret_cast<float *>(sm + F::OFF_L);  // [stage][lse, delta][128]
+              DSR = PR + 16, OUT = DSR + 16, DRAIN = OUT + 8;
+    float *s_stat = reinterpret_cast<float *>(sm + F::OFF_L);  // [stage][-lse, -delta][128]
     u32 *s_tmem = reinterpret_cast<u32 *>(sm + F::OFF_BAR + F::BARS * 8);
     volatile int *s_abort = reinterpret_cast<volatile int *>(sm + F::OFF_BAR + F::BARS * 8 + 4);
     constexpr unsigned long long TO = AB_TIMEOUT_NS;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int kvh = blockIdx.y, b = blockIdx.z;
     Entry e;
     if (!entry_of(p, b, e)) return;
@@ -429,8 +457,10 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::BARS; ++i) mbar_init(bar0 + 8 * i, 1);
-        mbar_init(PR, 256);
-        mbar_init(DSR, 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(PR + 8 * i, 256);
+            mbar_init(DSR + 8 * i, 256);
+        }
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -438,7 +468,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     tc_before();
     __syncthreads();
     tc_after();
-    const u32 tmem = *s_tmem;
+    const u32 tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
     const u32 s_col = tmem, dp_col = tmem + 128, dv_col = tmem + 256, dk_col = tmem + 384;
 
     if (warp == 0) {
@@ -450,7 +480,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             int u = 0;
             for (; u < n; ++u) {
                 const int s = u % ST, row = e.q0 + row_of(u), h = head_of(u);
-                if (u >= ST && !mbar_wait(QE + 8 * s, (u32)((u / ST) & 1) ^ 1, TO, s_abort)) {
+                if (u >= ST && !tc_wait(QE + 8 * s, (u32)((u / ST) & 1) ^ 1, TO, s_abort)) {
                     ok = false;
                     break;
                 }
@@ -462,68 +492,84 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 raise_device_error(DEVERR_TIMEOUT_PRODUCER);
                 *s_abort = 1;
             }
-            mbar_wait(KVF, 0, TO, nullptr);
-            for (int j = u - ST > 0 ? u - ST : 0; j < u; ++j) mbar_wait(QF + 8 * (j % ST), (u32)((j / ST) & 1), TO, nullptr);
+            tc_wait(KVF, 0, TO, nullptr);
+            for (int j = u - ST > 0 ? u - ST : 0; j < u; ++j) tc_wait(QF + 8 * (j % ST), (u32)((j / ST) & 1), TO, nullptr);
         }
     } else if (warp == 1) {
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             constexpr u32 ID_S = tc_idesc(128, false, false), ID_O = tc_idesc(DP, false, true);
-            bool ok = mbar_wait(KVF, 0, TO, s_abort);
-            auto form = [&](u32 d, u32 a, u32 bt) {
+            const bool leader = tc_elect();
+            bool ok = TC_WAIT_ALL(KVF, 0, TO, s_abort);
+            const u64 k_desc = tc_desc_k(sbase), v_desc = tc_desc_k(sbase + F::OFF_V), q_desc = tc_desc_k(sbase + F::OFF_Q),
+                      do_desc = tc_desc_k(sbase + F::OFF_DO), qt_desc = tc_desc_mn(sbase + F::OFF_Q),
+                      dot_desc = tc_desc_mn(sbase + F::OFF_DO);
+            auto stage = [&](int u) { return (u64)(u % ST * F::TILE >> 4); };
+            // columns 0 - 63 of P, dS are at the region's start, 64 - 127 at its column 64; the first half of each is
+            // ready first (part 0: steps 0, 1, 4, 5)
+            auto add = [&](u32 d, u32 a, u64 bt, int part, bool more) {
 #pragma unroll
-                for (int kk = 0; kk < DP / 16; ++kk) {
-                    const u32 at = (u32)(kk / 4) * TC_BLOCK + (kk % 4) * 32;
-                    tc_mma_ss(d, tc_desc_k(a + at), tc_desc_k(bt + at), ID_S, kk != 0);
+                for (int i = 0; i < 4; ++i) {
+                    const int kk = (i & 1) + (i >> 1) * 4 + 2 * part;
+                    tc_mma_ts(d, a + (kk / 4) * 64 + (kk % 4) * 8, bt + (u64)(kk * 2048 >> 4), ID_O,
+                              more || part != 0 || i != 0);
                 }
             };
-            // columns 0 - 63 of P, dS are at the region's start, 64 - 127 at its column 64
-            auto add = [&](u32 d, u32 a, u32 bt, bool more) {
+            auto add_when = [&](u32 bar, int u, u32 d, u32 a, u64 bt) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    tc_mma_ts(d, a + (kk / 4) * 64 + (kk % 4) * 8, tc_desc_mn(bt + kk * 2048), ID_O, more || kk != 0);
+                for (int part = 0; part < 2; ++part) {
+                    ok = ok && TC_WAIT_ALL(bar + 8 * part, (u32)(u & 1), TO, s_abort);
+                    if (!ok) return;
+                    tc_after();
+                    if (leader) add(d, a, bt, part, u != 0);
+                    __syncwarp();
+                }
             };
-            auto q_at = [&](int u) { return sbase + F::OFF_Q + u % ST * F::TILE; };
-            auto do_at = [&](int u) { return sbase + F::OFF_DO + u % ST * F::TILE; };
             auto q_ready = [&](int u) {
                 const u32 ph = (u32)((u / ST) & 1);
-                ok = ok && mbar_wait(QF + 8 * (u % ST), ph, TO, s_abort) && mbar_wait(LF + 8 * (u % ST), ph, TO, s_abort);
+                ok = ok && TC_WAIT_ALL(QF + 8 * (u % ST), ph, TO, s_abort) && TC_WAIT_ALL(LF + 8 * (u % ST), ph, TO, s_abort);
                 tc_after();
             };
             q_ready(0);
-            if (ok) {
-                form(s_col, sbase, q_at(0));
+            if (ok && leader) {
+                tc_gemm_nt<DP>(s_col, k_desc, q_desc + stage(0), ID_S);
                 tc_commit(SF);
-                form(dp_col, sbase + F::OFF_V, do_at(0));
+                tc_gemm_nt<DP>(dp_col, v_desc, do_desc + stage(0), ID_S);
                 tc_commit(DPF);
             }
+            __syncwarp();
             for (int u = 0; u < n && ok; ++u) {
-                ok = mbar_wait(PR, (u32)(u & 1), TO, s_abort);
+                add_when(PR, u, dv_col, s_col, dot_desc + stage(u));
                 if (!ok) break;
-                tc_after();
-                add(dv_col, s_col, do_at(u), u != 0);
                 if (u + 1 < n) {
                     q_ready(u + 1);
                     if (!ok) break;
-                    form(s_col, sbase, q_at(u + 1));
-                    tc_commit(SF);
+                    if (leader) {
+                        tc_gemm_nt<DP>(s_col, k_desc, q_desc + stage(u + 1), ID_S);
+                        tc_commit(SF);
+                    }
+                    __syncwarp();
                 }
-                ok = mbar_wait(DSR, (u32)(u & 1), TO, s_abort);
+                add_when(DSR, u, dk_col, dp_col, qt_desc + stage(u));
                 if (!ok) break;
-                tc_after();
-                add(dk_col, dp_col, q_at(u), u != 0);
-                tc_commit(QE + 8 * (u % ST));
-                if (u + 1 < n) {
-                    form(dp_col, sbase + F::OFF_V, do_at(u + 1));
-                    tc_commit(DPF);
+                if (leader) {
+                    tc_commit(QE + 8 * (u % ST));
+                    if (u + 1 < n) {
+                        tc_gemm_nt<DP>(dp_col, v_desc, do_desc + stage(u + 1), ID_S);
+                        tc_commit(DPF);
+                    }
                 }
+                __syncwarp();
             }
-            if (ok) tc_commit(OUT);
-            else {
+            if (!ok && lane == 0) {
                 raise_device_error(DEVERR_TIMEOUT_MMA);
                 *s_abort = 1;
             }
-            tc_commit(DRAIN);
-            mbar_wait(DRAIN, 0, TO, nullptr);
+            if (leader) {
+                if (ok) tc_commit(OUT);
+                tc_commit(DRAIN);
+            }
+            __syncwarp();
+            tc_wait(DRAIN, 0, TO, nullptr);
         }
     } else if (warp == 2) {
         // lse and delta of a query tile; rows behind the last query are cleared and get weights of zero
@@ -539,13 +585,13 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 lse[k] = r < rows ? p.lse[stat + r] : -INFINITY;
                 delta[k] = r < rows ? p.delta[stat + r] : 0.f;
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(QF + 8 * s, (u32)((u / ST) & 1), TO, s_abort));
+            ok = __all_sync(0xffffffffu, tc_wait(QF + 8 * s, (u32)((u / ST) & 1), TO, s_abort));
             if (!ok) break;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                // a query that sees nothing has lse = -inf: its weights are exp2(S - inf) = 0 as well
-                s_stat[(s * 2) * 128 + lane + 32 * k] = lse[k] == -INFINITY ? INFINITY : lse[k] * 1.44269504088896f;
-                s_stat[(s * 2 + 1) * 128 + lane + 32 * k] = delta[k];
+                // negated, to be added; a query that sees nothing has lse = -inf: its weights are exp2(S - inf) = 0 too
+                s_stat[(s * 2) * 128 + lane + 32 * k] = lse[k] == -INFINITY ? -INFINITY : lse[k] * -1.44269504088896f;
+                s_stat[(s * 2 + 1) * 128 + lane + 32 * k] = -delta[k];
             }
             if (rows < 128) {
                 tc_zero_rows<DP>(sm + F::OFF_Q + s * F::TILE, rows);
@@ -562,49 +608,52 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
         const int c = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;  // columns (queries) 64 c .. + 63 of key r
         const int key = j0 + r;
         const u32 lane_at = (u32)((warp & 3) * 32) << 16;
-        const float sl = p.scale_log2;
+        const f32x2 sl2 = pack2(p.scale_log2, p.scale_log2);
         bool ok = true;
         for (int u = 0; u < n; ++u) {
             const int s = u % ST, i0 = row_of(u);
-            ok = __all_sync(0xffffffffu, mbar_wait(LF + 8 * s, (u32)((u / ST) & 1), TO, s_abort) &&
-                                             mbar_wait(SF, (u32)(u & 1), TO, s_abort));
+            ok = __all_sync(0xffffffffu, tc_wait(LF + 8 * s, (u32)((u / ST) & 1), TO, s_abort) &&
+                                             tc_wait(SF, (u32)(u & 1), TO, s_abort));
             if (!ok) break;
             tc_after();
             u32 w[64];
             tc_ld32(w, s_col + lane_at + 64 * c);
             tc_ld32(w + 32, s_col + lane_at + 64 * c + 32);
-            const float4 *lse = reinterpret_cast<const float4 *>(s_stat + (s * 2) * 128 + 64 * c);
-            const float4 *del = reinterpret_cast<const float4 *>(s_stat + (s * 2 + 1) * 128 + 64 * c);
+            const float4 *nlse = reinterpret_cast<const float4 *>(s_stat + (s * 2) * 128 + 64 * c);
+            const float4 *ndel = reinterpret_cast<const float4 *>(s_stat + (s * 2 + 1) * 128 + 64 * c);
             tc_wait_ld();
             const int first = i0 + e.off;  // position of column 0
             const bool whole = j0 + 127 <= first && (p.window == 0 || first + 127 - j0 < p.window || j0 + 128 <= p.sinks);
-#pragma unroll
-            for (int j = 0; j < 64; j += 4) {
-                const float4 x = lse[j / 4];
-                w[j] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(w[j]), sl, -x.x)));
-                w[j + 1] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(w[j + 1]), sl, -x.y)));
-                w[j + 2] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(w[j + 2]), sl, -x.z)));
-                w[j + 3] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(w[j + 3]), sl, -x.w)));
-            }
-            if (!whole) {
-                const int lo = key - first - 64 * c;                                                 // first query
-                const int hi = p.window > 0 && key >= p.sinks ? lo + p.window : 0x7fffffff;  // behind the last one
-#pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    if (j < lo || j >= hi) w[j] = 0u;
-            }
+            const int lo = key - first - 64 * c;                                         // first query
+            const int hi = p.window > 0 && key >= p.sinks ? lo + p.window : 0x7fffffff;  // behind the last one
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
+                u32 *v = w + 32 * q;
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 x = nlse[8 * q + j / 4];
+                    float a, b2;
+                    unpack2(fma2(pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sl2, pack2(x.x, x.y)), a, b2);
+                    v[j] = __float_as_uint(exp2_fast(a));
+                    v[j + 1] = __float_as_uint(exp2_fast(b2));
+                    unpack2(fma2(pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), sl2, pack2(x.z, x.w)), a, b2);
+                    v[j + 2] = __float_as_uint(exp2_fast(a));
+                    v[j + 3] = __float_as_uint(exp2_fast(b2));
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (32 * q + j < lo || 32 * q + j >= hi) v[j] = 0u;
+                }
                 u32 pk[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    pk[j] = pack_bf16(__uint_as_float(w[32 * q + 2 * j]), __uint_as_float(w[32 * q + 2 * j + 1]));
+                for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
                 tc_st16(s_col + lane_at + 64 * c + 16 * q, pk);
+                tc_wait_st();
+                tc_before();
+                mbar_arrive(PR + 8 * q);
             }
-            tc_wait_st();
-            tc_before();
-            mbar_arrive(PR);
-            ok = __all_sync(0xffffffffu, mbar_wait(DPF, (u32)(u & 1), TO, s_abort));
+            ok = __all_sync(0xffffffffu, tc_wait(DPF, (u32)(u & 1), TO, s_abort));
             if (!ok) break;
             tc_after();
 #pragma unroll
@@ -614,19 +663,23 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 tc_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
-                    const float4 x = del[8 * q + j / 2];
-                    pk[j] = pack_bf16(__uint_as_float(w[32 * q + 2 * j]) * (__uint_as_float(g[2 * j]) - x.x),
-                                      __uint_as_float(w[32 * q + 2 * j + 1]) * (__uint_as_float(g[2 * j + 1]) - x.y));
-                    pk[j + 1] = pack_bf16(__uint_as_float(w[32 * q + 2 * j + 2]) * (__uint_as_float(g[2 * j + 2]) - x.z),
-                                          __uint_as_float(w[32 * q + 2 * j + 3]) * (__uint_as_float(g[2 * j + 3]) - x.w));
+                    const float4 x = ndel[8 * q + j / 2];
+                    const u32 *v = w + 32 * q + 2 * j;
+                    float a, b2;
+                    unpack2(mul2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                                 add2(pack2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1])), pack2(x.x, x.y))), a, b2);
+                    pk[j] = pack_bf16(a, b2);
+                    unpack2(mul2(pack2(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                                 add2(pack2(__uint_as_float(g[2 * j + 2]), __uint_as_float(g[2 * j + 3])), pack2(x.z, x.w))), a, b2);
+                    pk[j + 1] = pack_bf16(a, b2);
                 }
                 tc_st16(dp_col + lane_at + 64 * c + 16 * q, pk);
+                tc_wait_st();
+                tc_before();
+                mbar_arrive(DSR + 8 * q);
             }
-            tc_wait_st();
-            tc_before();
-            mbar_arrive(DSR);
         }
-        if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(OUT, 0, TO, s_abort));
+        if (ok && n > 0) ok = __all_sync(0xffffffffu, tc_wait(OUT, 0, TO, s_abort));
         if (!ok) {
             if (lane == 0) {
                 raise_device_error(DEVERR_TIMEOUT_EPILOGUE);
@@ -636,29 +689,32 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             tc_after();
             // the first four warps write dV, the others dK
             const float f = c == 0 ? 1.f : p.scale;
-            uint16_t *out = (c == 0 ? p.dv : p.dk) + ((size_t)(e.k0 + key) * p.Hkv + kvh) * p.D;
-            float *acc = nullptr;
-            if (to_sums)
-                acc = sums + sink_slot(cutting, p.Hkv, p.D, b, kvh, t, piece) + ((size_t)(c == 0 ? 1 : 0) * 128 + r) * p.D;
+            const u32 col = (c == 0 ? dv_col : dk_col) + lane_at;
+            if (!to_sums) {
+                // (the query stages are not read any more)
+                const int at = 32 * (warp & 3);
+                tc_store_rows<DP>(col, n == 0, f, sm + F::OFF_Q + (warp - 4) * 32 * DP * 2,
+                                  (c == 0 ? p.dv : p.dk) + ((size_t)(e.k0 + j0 + at) * p.Hkv + kvh) * p.D,
+                                  (long long)p.Hkv * p.D, keys - at, p.D);
+            } else {
+                float *acc = sums + sink_slot(cutting, p.Hkv, p.D, b, kvh, t, piece) + ((size_t)(c == 0 ? 1 : 0) * 128 + r) * p.D;
 #pragma unroll 1
-            for (int k = 0; k < DP / 32; ++k) {
-                u32 o[32];
-                if (n > 0) {
-                    tc_ld32(o, (c == 0 ? dv_col : dk_col) + lane_at + 32 * k);
-                    tc_wait_ld();
-                } else {
+                for (int k = 0; k < DP / 32; ++k) {
+                    u32 o[32];
+                    if (n > 0) {
+                        tc_ld32(o, col + 32 * k);
+                        tc_wait_ld();
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0u;
-                }
-                if (r < keys) {
+                        for (int j = 0; j < 32; ++j) o[j] = 0u;
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
-                        if (32 * k + j >= p.D) continue;
+                        if (r >= keys || 32 * k + j >= p.D) continue;
                         float x[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[j + i]) * f;
-                        if (to_sums) store8(reinterpret_cast<uint8_t *>(acc + 32 * k + j), x, false);
-                        else store8(reinterpret_cast<uint8_t *>(out + 32 * k + j), x, true);
+                        store8(reinterpret_cast<uint8_t *>(acc + 32 * k + j), x, false);
                     }
                 }
             }

@@ -32,13 +32,17 @@ namespace bl {
 constexpr int AF_THREADS = 384;
 constexpr int AF_ROWS = 256;
 constexpr int AF_KEYS = 128;
+// registers a thread: 168 at launch (the first warpgroup gives its share up,
+// the softmax warpgroups take it); what is taken, (64 + 2 x 208) x 128, is
+// checked against the kernel's own count before it is first launched
+constexpr int AF_REGS_LOW = 64, AF_REGS_HIGH = 208;
 
 template <int DP>
 struct FwdShape {
     static constexpr int STAGES = DP == 64 ? 4 : 2;
     static constexpr int TILE = DP / 64 * TC_BLOCK;  // 128 rows
     static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + STAGES * TILE, OFF_BAR = OFF_V + STAGES * TILE;
-    static constexpr int BARS = 2 + 4 * STAGES + 9;
+    static constexpr int BARS = 2 + 4 * STAGES + 11;
     static constexpr int SMEM = OFF_BAR + BARS * 8 + 16 + 1024;
 };
 
@@ -67,12 +71,12 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(af_raw) + 1023) & ~(uintptr_t)1023);
     const u32 sbase = smem_u32(sm), bar0 = sbase + F::OFF_BAR;
     const u32 QF = bar0, KF = bar0 + 16, KE = KF + 8 * ST, VF = KE + 8 * ST, VE = VF + 8 * ST, SF = VE + 8 * ST,
-              PF = SF + 16, OF = PF + 16, CUT = OF + 16, FIX = CUT + 8, DRAIN = FIX + 8;
+              PF = SF + 16, OF = PF + 32, CUT = OF + 16, FIX = CUT + 8, DRAIN = FIX + 8;
     u32 *s_tmem = reinterpret_cast<u32 *>(sm + F::OFF_BAR + F::BARS * 8);
     volatile int *s_abort = reinterpret_cast<volatile int *>(sm + F::OFF_BAR + F::BARS * 8 + 4);
     constexpr unsigned long long TO = 2000000000ull;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int h = blockIdx.y, b = blockIdx.z;
     if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) check_entry(p, b);
     Entry e;
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::BARS; ++i) mbar_init(bar0 + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(PF + 8 * i, 128);
+        for (int i = 0; i < 4; ++i) mbar_init(PF + 8 * i, 128);
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -101,7 +105,7 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
     tc_before();
     __syncthreads();
     tc_after();
-    const u32 tmem = *s_tmem;
+    const u32 tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
     // TMEM columns: S / P of the halves at 0 and 128, O at 256 and 256 + DP
     auto s_col = [&](int half) { return tmem + 128u * half; };
     auto o_col = [&](int half) { return tmem + 256u + (u32)DP * half; };
@@ -113,109 +117,126 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
     auto v_full = [&](int u) { return cuts && u == count - 1 ? CUT : VF + 8 * (u % ST); };
     auto v_phase = [&](int u) { return cuts && u == count - 1 ? 0u : (u32)((u / ST) & 1); };
 
-    if (warp == 0) {
-        if (lane == 0) {
-            bool failed = false;
-            for (int half = 0; half < 2; ++half) {
-                if (ht[half].last < 0) continue;
-                mbar_arrive_expect_tx(QF + 8 * half, F::TILE);
-                tc_load_rows<DP>(&maps.q, sbase + half * F::TILE, h, e.q0 + i0 + 128 * half, QF + 8 * half);
-            }
-            int u = 0;
-            for (; u < count; ++u) {
-                const int s = u % ST, row = e.k0 + tile_of(u) * AF_KEYS;
-                const u32 ph = (u32)((u / ST) & 1) ^ 1;
-                if (u >= ST && !(mbar_wait(KE + 8 * s, ph, TO, s_abort) && mbar_wait(VE + 8 * s, ph, TO, s_abort))) {
-                    failed = true;
-                    break;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(AF_REGS_LOW));
+        if (warp == 0) {
+            if (lane == 0) {
+                bool failed = false;
+                for (int half = 0; half < 2; ++half) {
+                    if (ht[half].last < 0) continue;
+                    mbar_arrive_expect_tx(QF + 8 * half, F::TILE);
+                    tc_load_rows<DP>(&maps.q, sbase + half * F::TILE, h, e.q0 + i0 + 128 * half, QF + 8 * half);
                 }
-                mbar_arrive_expect_tx(KF + 8 * s, F::TILE);
-                tc_load_rows<DP>(&maps.k, sbase + F::OFF_K + s * F::TILE, kvh, row, KF + 8 * s);
-                mbar_arrive_expect_tx(v_full(u), F::TILE);
-                tc_load_rows<DP>(&maps.v, sbase + F::OFF_V + s * F::TILE, kvh, row, v_full(u));
-            }
-            if (failed) {
-                raise_device_error(DEVERR_TIMEOUT_PRODUCER);
-                *s_abort = 1;
-            }
-            // what was requested lands before the CTA exits
-            for (int half = 0; half < 2; ++half)
-                if (ht[half].last >= 0) mbar_wait(QF + 8 * half, 0, TO, nullptr);
-            for (int j = u - ST > 0 ? u - ST : 0; j < u; ++j) {
-                mbar_wait(KF + 8 * (j % ST), (u32)((j / ST) & 1), TO, nullptr);
-                mbar_wait(v_full(j), v_phase(j), TO, nullptr);
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && count > 0) {
-            constexpr u32 ID_QK = tc_idesc(AF_KEYS, false, false), ID_PV = tc_idesc(DP, false, true);
-            bool ok = true;
-            int n[2] = {0, 0};  // tiles of a half whose P was consumed
-            int k_seen = -1, v_seen = -1;
-            auto qk = [&](int half, int u) {
-                const int s = u % ST;
-                if (k_seen < u) {
-                    ok = ok && mbar_wait(KF + 8 * s, (u32)((u / ST) & 1), TO, s_abort);
-                    k_seen = u;
-                }
-                if (n[half] == 0) ok = ok && mbar_wait(QF + 8 * half, 0, TO, s_abort);
-                if (!ok) return;
-                tc_after();
-                const u32 a = sbase + half * F::TILE, k = sbase + F::OFF_K + s * F::TILE;
-#pragma unroll
-                for (int kk = 0; kk < DP / 16; ++kk) {
-                    const u32 at = (u32)(kk / 4) * TC_BLOCK + (kk % 4) * 32;
-                    tc_mma_ss(s_col(half), tc_desc_k(a + at), tc_desc_k(k + at), ID_QK, kk != 0);
-                }
-                tc_commit(SF + 8 * half);
-            };
-            for (int half = 0; half < 2 && ok; ++half)
-                if (ht[half].has(tile_of(0))) qk(half, 0);
-            if (ok) tc_commit(KE);
-            for (int u = 0; u < count && ok; ++u) {
-                const int s = u % ST, t = tile_of(u);
-                for (int half = 0; half < 2 && ok; ++half) {
-                    if (ht[half].has(t)) {
-                        if (v_seen < u) {
-                            ok = ok && mbar_wait(t == cut_tile ? FIX : VF + 8 * s, v_phase(u), TO, s_abort);
-                            v_seen = u;
-                        }
-                        ok = ok && mbar_wait(PF + 8 * half, (u32)(n[half] & 1), TO, s_abort);
-                        if (!ok) break;
-                        tc_after();
-                        const u32 v = sbase + F::OFF_V + s * F::TILE;
-#pragma unroll
-                        for (int kk = 0; kk < AF_KEYS / 16; ++kk)
-                            tc_mma_ts(o_col(half), s_col(half) + 8 * kk, tc_desc_mn(v + kk * 2048), ID_PV,
-                                      n[half] != 0 || kk != 0);
-                        ++n[half];
-                        if (t == ht[half].last) tc_commit(OF + 8 * half);
+                int u = 0;
+                for (; u < count; ++u) {
+                    const int s = u % ST, row = e.k0 + tile_of(u) * AF_KEYS;
+                    const u32 ph = (u32)((u / ST) & 1) ^ 1;
+                    if (u >= ST && !(tc_wait(KE + 8 * s, ph, TO, s_abort) && tc_wait(VE + 8 * s, ph, TO, s_abort))) {
+                        failed = true;
+                        break;
                     }
-                    if (u + 1 < count && ht[half].has(tile_of(u + 1))) qk(half, u + 1);
+                    mbar_arrive_expect_tx(KF + 8 * s, F::TILE);
+                    tc_load_rows<DP>(&maps.k, sbase + F::OFF_K + s * F::TILE, kvh, row, KF + 8 * s);
+                    mbar_arrive_expect_tx(v_full(u), F::TILE);
+                    tc_load_rows<DP>(&maps.v, sbase + F::OFF_V + s * F::TILE, kvh, row, v_full(u));
                 }
-                if (!ok) break;
-                tc_commit(VE + 8 * s);
-                if (u + 1 < count) tc_commit(KE + 8 * ((u + 1) % ST));
+                if (failed) {
+                    raise_device_error(DEVERR_TIMEOUT_PRODUCER);
+                    *s_abort = 1;
+                }
+                // what was requested lands before the CTA exits
+                for (int half = 0; half < 2; ++half)
+                    if (ht[half].last >= 0) tc_wait(QF + 8 * half, 0, TO, nullptr);
+                for (int j = u - ST > 0 ? u - ST : 0; j < u; ++j) {
+                    tc_wait(KF + 8 * (j % ST), (u32)((j / ST) & 1), TO, nullptr);
+                    tc_wait(v_full(j), v_phase(j), TO, nullptr);
+                }
             }
-            if (!ok) {
-                raise_device_error(DEVERR_TIMEOUT_MMA);
-                *s_abort = 1;
+        } else if (warp == 1) {
+            if (count > 0) {
+                constexpr u32 ID_QK = tc_idesc(AF_KEYS, false, false), ID_PV = tc_idesc(DP, false, true);
+                const bool leader = tc_elect();
+                bool ok = true;
+                int n[2] = {0, 0};  // tiles of a half whose P was consumed
+                int k_seen = -1, v_seen = -1;
+                const u64 q_desc = tc_desc_k(sbase), k_desc = tc_desc_k(sbase + F::OFF_K), v_desc = tc_desc_mn(sbase + F::OFF_V);
+                auto qk = [&](int half, int u) {
+                    const int s = u % ST;
+                    if (k_seen < u) {
+                        ok = ok && TC_WAIT_ALL(KF + 8 * s, (u32)((u / ST) & 1), TO, s_abort);
+                        k_seen = u;
+                    }
+                    if (n[half] == 0) ok = ok && TC_WAIT_ALL(QF + 8 * half, 0, TO, s_abort);
+                    if (!ok) return;
+                    tc_after();
+                    if (leader) {
+                        tc_gemm_nt<DP>(s_col(half), q_desc + (u64)(half * F::TILE >> 4), k_desc + (u64)(s * F::TILE >> 4), ID_QK);
+                        tc_commit(SF + 8 * half);
+                    }
+                    __syncwarp();
+                };
+                for (int half = 0; half < 2 && ok; ++half)
+                    if (ht[half].has(tile_of(0))) qk(half, 0);
+                if (ok && leader) tc_commit(KE);
+                for (int u = 0; u < count && ok; ++u) {
+                    const int s = u % ST, t = tile_of(u);
+    #pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (ok && ht[half].has(t)) {
+                            if (v_seen < u) {
+                                ok = TC_WAIT_ALL(t == cut_tile ? FIX : VF + 8 * s, v_phase(u), TO, s_abort);
+                                v_seen = u;
+                            }
+                            const u64 v = v_desc + (u64)(s * F::TILE >> 4);
+                            // the weights of the first 64 keys are ready before the others
+    #pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+                                ok = ok && TC_WAIT_ALL(PF + 8 * (2 * half + part), (u32)(n[half] & 1), TO, s_abort);
+                                if (!ok) break;
+                                tc_after();
+                                if (leader) {
+    #pragma unroll
+                                    for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
+                                        tc_mma_ts(o_col(half), s_col(half) + 8 * kk, v + (u64)(kk * 2048 >> 4), ID_PV,
+                                                  n[half] != 0 || kk != 0);
+                                }
+                                __syncwarp();
+                            }
+                            if (!ok) break;
+                            ++n[half];
+                            if (t == ht[half].last && leader) tc_commit(OF + 8 * half);
+                        }
+                        if (ok && u + 1 < count && ht[half].has(tile_of(u + 1))) qk(half, u + 1);
+                    }
+                    if (!ok) break;
+                    if (leader) {
+                        tc_commit(VE + 8 * s);
+                        if (u + 1 < count) tc_commit(KE + 8 * ((u + 1) % ST));
+                    }
+                    __syncwarp();
+                }
+                if (!ok && lane == 0) {
+                    raise_device_error(DEVERR_TIMEOUT_MMA);
+                    *s_abort = 1;
+                }
+                // everything issued completes before TMEM is freed
+                if (leader) tc_commit(DRAIN);
+                __syncwarp();
+                tc_wait(DRAIN, 0, TO, nullptr);
             }
-            // everything issued completes before TMEM is freed
-            tc_commit(DRAIN);
-            mbar_wait(DRAIN, 0, TO, nullptr);
+        } else if (warp == 2) {
+            if (cuts) {
+                if (__all_sync(0xffffffffu, tc_wait(CUT, 0, TO, s_abort))) {
+                    tc_zero_rows<DP>(sm + F::OFF_V + (count - 1) % ST * F::TILE, cut);
+                    if (lane == 0) mbar_arrive(FIX);
+                } else if (lane == 0) {
+                    raise_device_error(DEVERR_TIMEOUT_EXPAND);
+                    *s_abort = 1;
+                }
+            }
         }
-    } else if (warp == 2) {
-        if (cuts) {
-            if (__all_sync(0xffffffffu, mbar_wait(CUT, 0, TO, s_abort))) {
-                tc_zero_rows<DP>(sm + F::OFF_V + (count - 1) % ST * F::TILE, cut);
-                if (lane == 0) mbar_arrive(FIX);
-            } else if (lane == 0) {
-                raise_device_error(DEVERR_TIMEOUT_EXPAND);
-                *s_abort = 1;
-            }
-        }
-    } else if (warp >= 4) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(AF_REGS_HIGH));
         const int half = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
         const int row = i0 + 128 * half + r, rows = half ? rows1 : rows0;
         const int pos = row + e.off;
@@ -229,7 +250,7 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
         for (int u = 0; u < count; ++u) {
             const int t = tile_of(u);
             if (!mine.has(t)) continue;
-            ok = __all_sync(0xffffffffu, mbar_wait(SF + 8 * half, (u32)(n & 1), TO, s_abort));
+            ok = __all_sync(0xffffffffu, tc_wait(SF + 8 * half, (u32)(n & 1), TO, s_abort));
             if (!ok) break;
             tc_after();
             u32 w[128];
@@ -237,20 +258,33 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
             for (int c = 0; c < 4; ++c) tc_ld32(w + 32 * c, s_col(half) + lane_at + 32 * c);
             tc_wait_ld();
             const int j0 = t * AF_KEYS;
-            // whole tile visible to every row of the half?
-            const bool whole = j0 + AF_KEYS - 1 <= first_pos && j0 + AF_KEYS <= e.nk &&
-                               (p.window == 0 || last_pos - j0 < p.window || j0 + AF_KEYS <= p.sinks);
-            if (!whole) {
-                const int lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 - j0 : 0;  // first key of the window
-                const int hi = (pos < e.nk - 1 ? pos : e.nk - 1) - j0;                        // last key
-                const int sk = p.sinks - j0;                                                  // keys below are sinks
+            // keys that some row of the half must not see: behind its position or the last key, or before its window
+            const bool cut_hi = j0 + AF_KEYS - 1 > first_pos || j0 + AF_KEYS > e.nk;
+            const bool cut_lo = p.window > 0 && last_pos - j0 >= p.window && j0 + AF_KEYS > p.sinks;
+            if (cut_hi) {
+                const int hi = (pos < e.nk - 1 ? pos : e.nk - 1) - j0;
 #pragma unroll
                 for (int j = 0; j < 128; ++j)
-                    if (j > hi || (j < lo && j >= sk)) w[j] = 0xff800000u;
+                    if (j > hi) w[j] = 0xff800000u;
             }
-            float mx = __uint_as_float(w[0]);
+            if (cut_lo) {
+                const int lo = pos - p.window + 1 - j0, sk = p.sinks - j0;
+                if (sk <= 0) {
 #pragma unroll
-            for (int j = 1; j < 128; ++j) mx = fmaxf(mx, __uint_as_float(w[j]));
+                    for (int j = 0; j < 128; ++j)
+                        if (j < lo) w[j] = 0xff800000u;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j < lo && j >= sk) w[j] = 0xff800000u;
+                }
+            }
+            float mq[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mq[j] = __uint_as_float(w[j]);
+#pragma unroll
+            for (int j = 8; j < 128; ++j) mq[j & 7] = fmaxf(mq[j & 7], __uint_as_float(w[j]));
+            const float mx = fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), fmaxf(fmaxf(mq[4], mq[5]), fmaxf(mq[6], mq[7])));
             if (__any_sync(0xffffffffu, (mx - m) * sl > 8.f || m == -INFINITY)) {
                 const float top = fmaxf(m, mx), c = m == -INFINITY ? 0.f : exp2_fast((m - top) * sl);
                 m = top;
@@ -268,27 +302,34 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
                 }
             }
             const float base = m == -INFINITY ? 0.f : m * sl;
-            float sum0 = 0.f, sum1 = 0.f;
+            const f32x2 sl2 = pack2(sl, sl), nb2 = pack2(-base, -base);
+            f32x2 sum[2] = {0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 u32 pk[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const float x = exp2_fast(fmaf(__uint_as_float(w[32 * c + 2 * j]), sl, -base));
-                    const float y = exp2_fast(fmaf(__uint_as_float(w[32 * c + 2 * j + 1]), sl, -base));
-                    sum0 += x;
-                    sum1 += y;
+                    float x, y;
+                    unpack2(fma2(pack2(__uint_as_float(w[32 * c + 2 * j]), __uint_as_float(w[32 * c + 2 * j + 1])), sl2, nb2), x, y);
+                    x = exp2_fast(x);
+                    y = exp2_fast(y);
+                    sum[j & 1] = add2(sum[j & 1], pack2(x, y));
                     pk[j] = pack_bf16(x, y);
                 }
                 tc_st16(s_col(half) + lane_at + 16 * c, pk);
+                if (c & 1) {
+                    tc_wait_st();
+                    tc_before();
+                    mbar_arrive(PF + 8 * (2 * half + (c >> 1)));
+                }
             }
-            l += sum0 + sum1;
-            tc_wait_st();
-            tc_before();
-            mbar_arrive(PF + 8 * half);
+            float x0, x1, x2, x3;
+            unpack2(sum[0], x0, x1);
+            unpack2(sum[1], x2, x3);
+            l += (x0 + x1) + (x2 + x3);
             ++n;
         }
-        if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(OF + 8 * half, 0, TO, s_abort));
+        if (ok && n > 0) ok = __all_sync(0xffffffffu, tc_wait(OF + 8 * half, 0, TO, s_abort));
         if (!ok) {
             if (lane == 0) {
                 raise_device_error(DEVERR_TIMEOUT_EPILOGUE);
@@ -297,29 +338,11 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
         } else if (rows > 0) {
             tc_after();
             const float f = l > 0.f ? 1.f / l : 0.f;
-            uint16_t *out = p.o + ((size_t)(e.q0 + row) * p.Hq + h) * p.D;
-#pragma unroll 1
-            for (int k = 0; k < DP / 32; ++k) {
-                u32 o[32];
-                if (n > 0) {
-                    tc_ld32(o, o_col(half) + lane_at + 32 * k);
-                    tc_wait_ld();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0u;
-                }
-                if (r < rows) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        if (32 * k + j < p.D)
-                            *reinterpret_cast<uint4 *>(out + 32 * k + j) =
-                                make_uint4(pack_bf16(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f),
-                                           pack_bf16(__uint_as_float(o[j + 2]) * f, __uint_as_float(o[j + 3]) * f),
-                                           pack_bf16(__uint_as_float(o[j + 4]) * f, __uint_as_float(o[j + 5]) * f),
-                                           pack_bf16(__uint_as_float(o[j + 6]) * f, __uint_as_float(o[j + 7]) * f));
-                    }
-                }
-            }
+            // (the half's Q tile is not read any more)
+            const int first = 32 * (warp & 3);
+            tc_store_rows<DP>(o_col(half) + lane_at, n == 0, f, sm + half * F::TILE + first * DP * 2,
+                              p.o + ((size_t)(e.q0 + i0 + 128 * half + first) * p.Hq + h) * p.D, (long long)p.Hq * p.D,
+                              rows - first, p.D);
             if (r < rows)
                 p.lse[(size_t)h * p.Tq + e.q0 + row] = l > 0.f ? m * p.scale + logf(l) : -INFINITY;
         }
