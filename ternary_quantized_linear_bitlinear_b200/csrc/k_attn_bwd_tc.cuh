@@ -112,37 +112,34 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             mbar_arrive_expect_tx(QF, 2 * F::TILE);
             tc_load_rows<DP>(&maps.q, sbase, h, e.q0 + i0, QF);
             tc_load_rows<DP>(&maps.dout, sbase + F::OFF_DO, h, e.q0 + i0, QF);
-            int u = 0;
+            int u = 0, ku = 0;  // tiles of V and of K requested
             for (; u < n; ++u) {
                 const int ks = u % KS, vs = u % VS, row = e.k0 + tile_of(u) * AF_KEYS;
-                if (u >= KS) ok = ok && tc_wait(KE + 8 * ks, (u32)((u / KS) & 1) ^ 1, TO, s_abort);
-                if (u >= VS) ok = ok && tc_wait(VE + 8 * vs, (u32)((u / VS) & 1) ^ 1, TO, s_abort);
-                if (!ok) break;
-                if (cuts && u == n - 1) {
-                    mbar_arrive_expect_tx(CUT, 2 * F::TILE);
-                    tc_load_rows<DP>(&maps.k, sbase + F::OFF_K + ks * F::TILE, kvh, row, CUT);
-                    tc_load_rows<DP>(&maps.v, sbase + F::OFF_V + vs * F::TILE, kvh, row, CUT);
-                } else {
-                    mbar_arrive_expect_tx(KF + 8 * ks, F::TILE);
-                    tc_load_rows<DP>(&maps.k, sbase + F::OFF_K + ks * F::TILE, kvh, row, KF + 8 * ks);
-                    mbar_arrive_expect_tx(VF + 8 * vs, F::TILE);
-                    tc_load_rows<DP>(&maps.v, sbase + F::OFF_V + vs * F::TILE, kvh, row, VF + 8 * vs);
-                }
+                const bool last = cuts && u == n - 1;
+                if (u >= KS && !tc_wait(KE + 8 * ks, (u32)((u / KS) & 1) ^ 1, TO, s_abort)) break;
+                const u32 kbar = last ? CUT : KF + 8 * ks, vbar = last ? CUT : VF + 8 * vs;
+                mbar_arrive_expect_tx(kbar, last ? 2 * F::TILE : F::TILE);
+                tc_load_rows<DP>(&maps.k, sbase + F::OFF_K + ks * F::TILE, kvh, row, kbar);
+                ku = u + 1;
+                if (u >= VS && !tc_wait(VE + 8 * vs, (u32)((u / VS) & 1) ^ 1, TO, s_abort)) break;
+                if (!last) mbar_arrive_expect_tx(vbar, F::TILE);
+                tc_load_rows<DP>(&maps.v, sbase + F::OFF_V + vs * F::TILE, kvh, row, vbar);
             }
+            ok = u == n;
             if (!ok) {
                 raise_device_error(DEVERR_TIMEOUT_PRODUCER);
                 *s_abort = 1;
             }
             // what was requested lands before the CTA exits
             tc_wait(QF, 0, TO, nullptr);
-            for (int j = u - KS > 0 ? u - KS : 0; j < u; ++j) {
-                if (cuts && j == n - 1) {
-                    tc_wait(CUT, 0, TO, nullptr);
-                } else {
-                    tc_wait(KF + 8 * (j % KS), (u32)((j / KS) & 1), TO, nullptr);
-                    if (j >= u - VS) tc_wait(VF + 8 * (j % VS), (u32)((j / VS) & 1), TO, nullptr);
-                }
+            // (a last tile of which only K was requested does not complete its barrier: that wait runs its time out,
+            // and K has landed by then)
+            for (int j = ku - KS > 0 ? ku - KS : 0; j < ku; ++j) {
+                if (cuts && j == n - 1) tc_wait(CUT, 0, TO, nullptr);
+                else tc_wait(KF + 8 * (j % KS), (u32)((j / KS) & 1), TO, nullptr);
             }
+            for (int j = u - VS > 0 ? u - VS : 0; j < u; ++j)
+                if (!(cuts && j == n - 1)) tc_wait(VF + 8 * (j % VS), (u32)((j / VS) & 1), TO, nullptr);
         }
     } else if (warp == 1) {
         if (n > 0) {

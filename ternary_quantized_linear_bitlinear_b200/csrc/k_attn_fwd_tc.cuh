@@ -127,16 +127,22 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
                     mbar_arrive_expect_tx(QF + 8 * half, F::TILE);
                     tc_load_rows<DP>(&maps.q, sbase + half * F::TILE, h, e.q0 + i0 + 128 * half, QF + 8 * half);
                 }
-                int u = 0;
+                int u = 0, ks = 0;  // tiles of V and of K requested
                 for (; u < count; ++u) {
                     const int s = u % ST, row = e.k0 + tile_of(u) * AF_KEYS;
                     const u32 ph = (u32)((u / ST) & 1) ^ 1;
-                    if (u >= ST && !(tc_wait(KE + 8 * s, ph, TO, s_abort) && tc_wait(VE + 8 * s, ph, TO, s_abort))) {
+                    // (K is wanted a step before V, and its stage is free that much earlier)
+                    if (u >= ST && !tc_wait(KE + 8 * s, ph, TO, s_abort)) {
                         failed = true;
                         break;
                     }
                     mbar_arrive_expect_tx(KF + 8 * s, F::TILE);
                     tc_load_rows<DP>(&maps.k, sbase + F::OFF_K + s * F::TILE, kvh, row, KF + 8 * s);
+                    ks = u + 1;
+                    if (u >= ST && !tc_wait(VE + 8 * s, ph, TO, s_abort)) {
+                        failed = true;
+                        break;
+                    }
                     mbar_arrive_expect_tx(v_full(u), F::TILE);
                     tc_load_rows<DP>(&maps.v, sbase + F::OFF_V + s * F::TILE, kvh, row, v_full(u));
                 }
@@ -147,10 +153,9 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
                 // what was requested lands before the CTA exits
                 for (int half = 0; half < 2; ++half)
                     if (ht[half].last >= 0) tc_wait(QF + 8 * half, 0, TO, nullptr);
-                for (int j = u - ST > 0 ? u - ST : 0; j < u; ++j) {
+                for (int j = ks - ST > 0 ? ks - ST : 0; j < ks; ++j)
                     tc_wait(KF + 8 * (j % ST), (u32)((j / ST) & 1), TO, nullptr);
-                    tc_wait(v_full(j), v_phase(j), TO, nullptr);
-                }
+                for (int j = u - ST > 0 ? u - ST : 0; j < u; ++j) tc_wait(v_full(j), v_phase(j), TO, nullptr);
             }
         } else if (warp == 1) {
             if (count > 0) {
