@@ -71,6 +71,12 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     constexpr unsigned long long TO = AB_TIMEOUT_NS;
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        tc_prefetch(&maps.q);
+        tc_prefetch(&maps.k);
+        tc_prefetch(&maps.v);
+        tc_prefetch(&maps.dout);
+    }
     const int h = blockIdx.y, b = blockIdx.z;
     if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) check_entry(p, b);
     Entry e;
@@ -97,6 +103,11 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
         mbar_init(DSR + 8, 256);
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (n > 0) {  // on their way while TMEM is allocated
+            mbar_arrive_expect_tx(QF, 2 * F::TILE);
+            tc_load_rows<DP>(&maps.q, sbase, h, e.q0 + i0, QF);
+            tc_load_rows<DP>(&maps.dout, sbase + F::OFF_DO, h, e.q0 + i0, QF);
+        }
     }
     if (warp == 1) tc_alloc(smem_u32(s_tmem), 512);
     tc_before();
@@ -109,9 +120,6 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     if (warp == 0) {
         if (lane == 0 && n > 0) {
             bool ok = true;
-            mbar_arrive_expect_tx(QF, 2 * F::TILE);
-            tc_load_rows<DP>(&maps.q, sbase, h, e.q0 + i0, QF);
-            tc_load_rows<DP>(&maps.dout, sbase + F::OFF_DO, h, e.q0 + i0, QF);
             int u = 0, ku = 0;  // tiles of V and of K requested
             for (; u < n; ++u) {
                 const int ks = u % KS, vs = u % VS, row = e.k0 + tile_of(u) * AF_KEYS;
@@ -422,6 +430,12 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     constexpr unsigned long long TO = AB_TIMEOUT_NS;
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        tc_prefetch(&maps.q);
+        tc_prefetch(&maps.k);
+        tc_prefetch(&maps.v);
+        tc_prefetch(&maps.dout);
+    }
     const int kvh = blockIdx.y, b = blockIdx.z;
     Entry e;
     if (!entry_of(p, b, e)) return;
@@ -460,6 +474,11 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
         }
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (n > 0) {  // on their way while TMEM is allocated
+            mbar_arrive_expect_tx(KVF, 2 * F::TILE);
+            tc_load_rows<DP>(&maps.k, sbase, kvh, e.k0 + j0, KVF);
+            tc_load_rows<DP>(&maps.v, sbase + F::OFF_V, kvh, e.k0 + j0, KVF);
+        }
     }
     if (warp == 1) tc_alloc(smem_u32(s_tmem), 512);
     tc_before();
@@ -471,9 +490,6 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     if (warp == 0) {
         if (lane == 0 && n > 0) {
             bool ok = true;
-            mbar_arrive_expect_tx(KVF, 2 * F::TILE);
-            tc_load_rows<DP>(&maps.k, sbase, kvh, e.k0 + j0, KVF);
-            tc_load_rows<DP>(&maps.v, sbase + F::OFF_V, kvh, e.k0 + j0, KVF);
             int u = 0;
             for (; u < n; ++u) {
                 const int s = u % ST, row = e.q0 + row_of(u), h = head_of(u);

@@ -77,6 +77,11 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
     constexpr unsigned long long TO = 2000000000ull;
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        tc_prefetch(&maps.q);
+        tc_prefetch(&maps.k);
+        tc_prefetch(&maps.v);
+    }
     const int h = blockIdx.y, b = blockIdx.z;
     if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) check_entry(p, b);
     Entry e;
@@ -100,6 +105,12 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
         for (int i = 0; i < 4; ++i) mbar_init(PF + 8 * i, 128);
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        // Q is on its way while TMEM is allocated
+        for (int half = 0; half < 2; ++half) {
+            if (ht[half].last < 0) continue;
+            mbar_arrive_expect_tx(QF + 8 * half, F::TILE);
+            tc_load_rows<DP>(&maps.q, sbase + half * F::TILE, h, e.q0 + i0 + 128 * half, QF + 8 * half);
+        }
     }
     if (warp == 1) tc_alloc(smem_u32(s_tmem), 512);
     tc_before();
@@ -122,11 +133,6 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
         if (warp == 0) {
             if (lane == 0) {
                 bool failed = false;
-                for (int half = 0; half < 2; ++half) {
-                    if (ht[half].last < 0) continue;
-                    mbar_arrive_expect_tx(QF + 8 * half, F::TILE);
-                    tc_load_rows<DP>(&maps.q, sbase + half * F::TILE, h, e.q0 + i0 + 128 * half, QF + 8 * half);
-                }
                 int u = 0, ks = 0;  // tiles of V and of K requested
                 for (; u < count; ++u) {
                     const int s = u % ST, row = e.k0 + tile_of(u) * AF_KEYS;

@@ -143,6 +143,10 @@ __device__ __forceinline__ void tc_st16(u32 addr, const u32 *r) {
         : "memory");
 }
 
+__device__ __forceinline__ void tc_prefetch(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // 128 rows x DP columns of one head of a [T, H, D] tensor (map: D, H, T) into
 // DP / 64 blocks; rows and columns beyond the tensor are zero.
 template <int DP>
