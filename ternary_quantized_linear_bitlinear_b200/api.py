@@ -594,20 +594,24 @@ def bl_linear_grouped(Ws, X, subln_gain=None, subln_eps: float = 1e-6, Ys=None, 
 # goes through the checks that say what is wrong with it.
 
 _Tensor = torch.Tensor
+_B16 = torch.bfloat16
+_I32 = torch.int32
 
 
 def _ok(t, dtype, cur: int) -> bool:
-    return isinstance(t, _Tensor) and t.is_cuda and t.get_device() == cur and t.dtype is dtype and t.is_contiguous()
+    # (get_device() is -1 for a CPU tensor)
+    return isinstance(t, _Tensor) and t.get_device() == cur and t.dtype is dtype and t.is_contiguous()
 
 
 def _rows3(t, name: str, cur: int, heads: int | None = None, D: int | None = None, dtype=None, rows: int | None = None):
     """Rows of heads [T, H, D] on the current device whose heads are contiguous
     (a row may be part of a wider one) -> row stride in elements."""
-    if isinstance(t, _Tensor) and t.is_cuda and t.get_device() == cur and t.dim() == 3 and t.dtype in _DTYPES:
+    if isinstance(t, _Tensor) and t.get_device() == cur and len(t.shape) == 3:
         T, H, d = t.shape
         st, sh, sd = t.stride()
-        if ((dtype is None or t.dtype is dtype) and (rows is None or T == rows) and (heads is None or H == heads)
-                and (D is None or d == D) and sd == 1 and (sh == d or H == 1)):
+        dt = t.dtype
+        if (sd == 1 and (sh == d or H == 1) and (dt is dtype or (dtype is None and dt in _DTYPES))
+                and (rows is None or T == rows) and (heads is None or H == heads) and (D is None or d == D)):
             if T == 1:
                 return H * d
             if st >= H * d:
@@ -654,14 +658,14 @@ def _i32(t, name: str, numel: int, cur: int):
 def _tables2(tables, lengths, refs, cur: int):
     """Checked tables [max_seqs, max_pages], lengths [max_seqs] and refs
     [num_pages] (either may be None) -> (max_seqs, max_pages)."""
-    if not (_ok(tables, torch.int32, cur) and tables.dim() == 2):
+    if not (_ok(tables, _I32, cur) and len(tables.shape) == 2):
         _dev(tables, "tables", torch.int32)
         if tables.dim() != 2:
             raise ValueError("tables must be 2-D [max_seqs, max_pages]")
     max_seqs, max_pages = tables.shape
-    if lengths is not None:
+    if lengths is not None and not (_ok(lengths, _I32, cur) and lengths.numel() == max_seqs):
         _i32(lengths, "lengths", max_seqs, cur)
-    if refs is not None and not (_ok(refs, torch.int32, cur) and refs.dim() == 1):
+    if refs is not None and not (_ok(refs, _I32, cur) and len(refs.shape) == 1):
         _dev(refs, "refs", torch.int32)
         if refs.dim() != 1:
             raise ValueError("refs must be 1-D [num_pages]")
@@ -672,8 +676,10 @@ def _kv_cache(k_pages, v_pages, tables, lengths, heads, D: int, cur: int):
     """The bytes of a bl_kv_cache of checked pages [num_pages, Hkv, page_size, D]
     and tables -> (bytes, Hkv, max_seqs)."""
     dt = k_pages.dtype if isinstance(k_pages, _Tensor) else None
-    if not (dt in _DTYPES and _ok(k_pages, dt, cur) and _ok(v_pages, dt, cur) and k_pages.dim() == 4
-            and v_pages.shape == k_pages.shape):
+    shape = k_pages.shape if dt in _DTYPES else ()
+    if not (len(shape) == 4 and isinstance(v_pages, _Tensor) and k_pages.get_device() == cur
+            and v_pages.get_device() == cur and v_pages.dtype is dt and v_pages.shape == shape
+            and k_pages.is_contiguous() and v_pages.is_contiguous()):
         _dev(k_pages, "k_pages")
         if k_pages.dim() != 4:
             raise ValueError("k_pages must be 4-D [num_pages, Hkv, page_size, D]")
@@ -682,7 +688,8 @@ def _kv_cache(k_pages, v_pages, tables, lengths, heads, D: int, cur: int):
         _dev(v_pages, "v_pages", dt)
         if v_pages.shape != k_pages.shape:
             raise ValueError("k_pages and v_pages must have the same shape")
-    pages, Hkv, ps, d = k_pages.shape
+        shape = k_pages.shape
+    pages, Hkv, ps, d = shape
     if heads is not None and Hkv != heads:
         raise ValueError(f"the pages have {Hkv} heads, expected {heads}")
     if d != D:
@@ -751,7 +758,7 @@ def bl_rope_append(q=None, k=None, v=None, rope=None, cu_seqlens=None, lengths=N
         raise ValueError(f"{B} batch entries, but lengths holds {max_seqs} sequences")
     if q is not None:
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=odt, device=q.device)
+            q_out = q.new_empty((T, Hq, D)) if odt is dt else q.new_empty((T, Hq, D), dtype=odt)
         else:
             _buf(q_out, "q_out", odt, T * Hq * D, cur)
     elif q_out is not None:
@@ -761,8 +768,8 @@ def bl_rope_append(q=None, k=None, v=None, rope=None, cu_seqlens=None, lengths=N
             raise ValueError("k_out or v_out without k and v")
     else:
         if (cache is None) if keep_kv is None else keep_kv:
-            k_out = torch.empty((T, Hkv, D), dtype=odt, device=k.device) if k_out is None else k_out
-            v_out = torch.empty((T, Hkv, D), dtype=odt, device=k.device) if v_out is None else v_out
+            k_out = k.new_empty((T, Hkv, D), dtype=odt) if k_out is None else k_out
+            v_out = k.new_empty((T, Hkv, D), dtype=odt) if v_out is None else v_out
         if k_out is not None:
             _buf(k_out, "k_out", odt, T * Hkv * D, cur)
         if v_out is not None:
@@ -796,23 +803,22 @@ def bl_attn_decode(q, k_pages, v_pages, tables, lengths, seq_ids=None, window: i
         _i32(seq_ids, "seq_ids", B, cur)
     elif B > max_seqs:
         raise ValueError(f"{B} batch entries, but the tables hold {max_seqs} sequences")
-    dev = q.device
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=q.dtype, device=dev)
+        out = q.new_empty((B, Hq, D))
     else:
         _buf(out, "out", q.dtype, B * Hq * D, cur)
     if lse is not None:
         _buf(lse, "lse", torch.float32, B * Hq, cur)
     elif return_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = q.new_empty((B, Hq), dtype=torch.float32)
     L = lib()
     if workspace is None:
-        workspace = torch.empty(L.bl_attn_decode_workspace_bytes(B, Hq, Hkv, D) or 16, dtype=torch.uint8, device=dev)
+        workspace = tables.new_empty(L.bl_attn_decode_workspace_bytes(B, Hq, Hkv, D) // 4 or 16)
     else:
         _buf(workspace, "workspace", torch.uint8, 1, cur)
     rc = L.bl_attn_decode(q.data_ptr(), _DTYPES[q.dtype], qs, B, Hq, Hkv, D, cache, _ptr(seq_ids), window, sinks,
-                          D ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.numel(),
-                          out.data_ptr(), _ptr(lse), _stream(stream))
+                          D ** -0.5 if scale is None else scale, workspace.data_ptr(),
+                          workspace.numel() * workspace.element_size(), out.data_ptr(), _ptr(lse), _stream(stream))
     if rc:
         _check(rc, "bl_attn_decode")
     return (out, lse) if return_lse else out
@@ -820,7 +826,7 @@ def bl_attn_decode(q, k_pages, v_pages, tables, lengths, seq_ids=None, window: i
 
 def _status(status, like, cur: int):
     if status is None:
-        return torch.empty(1, dtype=torch.int32, device=like.device)
+        return like.new_empty(1)
     _buf(status, "status", torch.int32, 1, cur)
     return status
 
@@ -882,12 +888,12 @@ def bl_kv_fork(pool, tables, lengths, refs, src, dst, status=None, workspace=Non
     status = _status(status, tables, cur)
     L = lib()
     if workspace is None:
-        workspace = torch.empty(L.bl_kv_fork_workspace_bytes(n) or 16, dtype=torch.uint8, device=tables.device)
+        workspace = tables.new_empty(L.bl_kv_fork_workspace_bytes(n) // 4 or 4)
     else:
         _buf(workspace, "workspace", torch.uint8, 1, cur)
     rc = L.bl_kv_fork(pool.data_ptr(), planes, page_bytes, tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(),
-                      refs.numel(), ps, max_seqs, max_pages, a, b, n, workspace.data_ptr(), workspace.numel(),
-                      status.data_ptr(), _stream(stream))
+                      refs.numel(), ps, max_seqs, max_pages, a, b, n, workspace.data_ptr(),
+                      workspace.numel() * workspace.element_size(), status.data_ptr(), _stream(stream))
     if rc:
         _check(rc, "bl_kv_fork")
     return status
@@ -900,17 +906,18 @@ def bl_kv_compact(pool, tables, refs, n_live=None, workspace=None, stream=None):
     max_seqs, max_pages = _tables2(tables, None, refs, cur)
     planes, page_bytes, _ = _pool(pool, refs, cur)
     if n_live is None:
-        n_live = torch.empty(1, dtype=torch.int32, device=tables.device)
+        n_live = tables.new_empty(1)
     else:
         _buf(n_live, "n_live", torch.int32, 1, cur)
     L = lib()
     pages = refs.numel()
     if workspace is None:
-        workspace = torch.empty(L.bl_kv_compact_workspace_bytes(pages) or 16, dtype=torch.uint8, device=tables.device)
+        workspace = tables.new_empty(L.bl_kv_compact_workspace_bytes(pages) // 4 or 4)
     else:
         _buf(workspace, "workspace", torch.uint8, 1, cur)
     rc = L.bl_kv_compact(pool.data_ptr(), planes, page_bytes, tables.data_ptr(), refs.data_ptr(), pages, max_seqs,
-                         max_pages, workspace.data_ptr(), workspace.numel(), n_live.data_ptr(), _stream(stream))
+                         max_pages, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                         n_live.data_ptr(), _stream(stream))
     if rc:
         _check(rc, "bl_kv_compact")
     return n_live
@@ -938,11 +945,11 @@ def bl_attn_forward(q, k, v, cu_q, cu_k, max_q: int, max_k: int, window: int = 0
     cur = _current_device()
     strides, (Tq, Tk, Hq, Hkv, D), (a, b, B) = _ragged(q, k, v, cu_q, cu_k, cur)
     if o is None:
-        o = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
+        o = q.new_empty((Tq, Hq, D))
     else:
         _buf(o, "o", torch.bfloat16, Tq * Hq * D, cur)
     if lse is None:
-        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((Hq, Tq), dtype=torch.float32)
     else:
         _buf(lse, "lse", torch.float32, Hq * Tq, cur)
     rc = lib().bl_attn_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, Tq, Tk, Hq, Hkv, D, a, b, B, max_q,
@@ -964,29 +971,28 @@ def bl_attn_backward(do, q, k, v, o, lse, cu_q, cu_k, max_q: int, max_k: int, wi
     dos = _rows3(do, "do", cur, heads=Hq, D=D, dtype=b16, rows=Tq)
     _buf(o, "o", b16, Tq * Hq * D, cur)
     _buf(lse, "lse", torch.float32, Hq * Tq, cur)
-    dev = q.device
     if dq is None:
-        dq = torch.empty((Tq, Hq, D), dtype=b16, device=dev)
+        dq = q.new_empty((Tq, Hq, D))
     else:
         _buf(dq, "dq", b16, Tq * Hq * D, cur)
     if dk is None:
-        dk = torch.empty((Tk, Hkv, D), dtype=b16, device=dev)
+        dk = k.new_empty((Tk, Hkv, D))
     else:
         _buf(dk, "dk", b16, Tk * Hkv * D, cur)
     if dv is None:
-        dv = torch.empty((Tk, Hkv, D), dtype=b16, device=dev)
+        dv = v.new_empty((Tk, Hkv, D))
     else:
         _buf(dv, "dv", b16, Tk * Hkv * D, cur)
     L = lib()
     if workspace is None:
         need = L.bl_attn_backward_workspace_bytes(Tq, Tk, Hq, Hkv, D, B, max_q, max_k, window, sinks)
-        workspace = torch.empty(need or 16, dtype=torch.uint8, device=dev)
+        workspace = cu_q.new_empty(need // 4 or 4)
     else:
         _buf(workspace, "workspace", torch.uint8, 1, cur)
     rc = L.bl_attn_backward(do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dos,
                             *strides, Tq, Tk, Hq, Hkv, D, a, b, B, max_q, max_k, window, sinks,
-                            D ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.numel(),
-                            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _stream(stream))
+                            D ** -0.5 if scale is None else scale, workspace.data_ptr(),
+                            workspace.numel() * workspace.element_size(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _stream(stream))
     if rc:
         _check(rc, "bl_attn_backward")
     return dq, dk, dv
