@@ -201,8 +201,8 @@ bl_status launch_decode(DecodeAttnParams &P, const AttnDevice &d, int64_t batche
     }
     k_attn_decode<C><<<ctas, C::WARPS * 32, ad_smem<C>(P.gsize), st>>>(P);
     if (cudaGetLastError() != cudaSuccess) return BL_ERR_CUDA;
-    return launch_after(k_attn_join<C::DP>, dim3((unsigned)P.B, (unsigned)P.Hq), AD_JOIN_THREADS, 0, st, P,
-                        ctas, C::WARPS);
+    if (ctas == 1) return BL_OK;  // nothing spans CTAs
+    return launch_after(k_attn_join<C::DP>, dim3((unsigned)ctas - 1, (unsigned)P.gsize), AD_JOIN_THREADS, 0, st, P);
 }
 
 template <int DP>
@@ -289,7 +289,7 @@ size_t bl_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_
     if (B < 1 || B > AD_MAX_B || check_heads(Hq, Hkv, D) != BL_OK) return 0;
     int parts, gsize;
     head_groups(Hq / Hkv, &parts, &gsize);
-    return align256((size_t)(B + 1) * 8) + (size_t)2 * AD_MAX_CTAS * gsize * ((D <= 64 ? 64 : 128) + 2) * 4;
+    return align256((size_t)AD_MAX_CTAS * 32) + (size_t)2 * AD_MAX_CTAS * gsize * ((D <= 64 ? 64 : 128) + 2) * 4;
 }
 
 bl_status bl_attn_decode(const void *q, bl_dtype xdt, int64_t q_stride, int64_t B, int64_t Hq, int64_t Hkv,
@@ -326,8 +326,8 @@ bl_status bl_attn_decode(const void *q, bl_dtype xdt, int64_t q_stride, int64_t 
     P.scale_log2 = scale * LOG2E;
     P.out = reinterpret_cast<uint8_t *>(out);
     P.lse = lse;
-    P.cum = reinterpret_cast<long long *>(workspace);
-    P.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + align256((size_t)(B + 1) * 8));
+    P.open = reinterpret_cast<long long *>(workspace);
+    P.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + align256((size_t)AD_MAX_CTAS * 32));
     AttnDevice *d;
     if ((rc = attn_device(&d))) return rc;
     // the line of batches at most, for small calls (8 keys per batch is the least)
@@ -556,7 +556,7 @@ bl_status bl_attn_backward(const void *do_, const void *q, const void *k, const 
         k_attn_dkdv_tc<128><<<gk, AB_THREADS, DkvShape<128>::SMEM, st>>>(maps, P, cut, sums);
     }
     if (cut.sink_tiles > 0)
-        k_attn_sink_sum<<<dim3((unsigned)cut.sink_tiles, (unsigned)Hkv, (unsigned)B), 256, 0, st>>>(P, cut, sums);
+        k_attn_sink_sum<<<dim3((unsigned)(cut.sink_tiles * AB_SUM_CTAS), (unsigned)Hkv, (unsigned)B), 256, 0, st>>>(P, cut, sums);
     return cudaGetLastError() == cudaSuccess ? BL_OK : BL_ERR_CUDA;
 }
 

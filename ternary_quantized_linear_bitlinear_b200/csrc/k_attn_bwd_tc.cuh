@@ -741,11 +741,14 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     }
 }
 
-// Sink tiles: the pieces' float32 sums, in order, to dk and dv.  One CTA per
-// (sink tile, kv head, entry).
+// Sink tiles: the pieces' float32 sums, in order, to dk and dv.  AB_SUM_CTAS
+// CTAs per (sink tile, kv head, entry): latency decides, so a thread adds up
+// one or two places.
+constexpr int AB_SUM_CTAS = 8;
+
 __global__ void __launch_bounds__(256) k_attn_sink_sum(const __grid_constant__ RaggedParams p,
                                                        const __grid_constant__ DkvCut cutting, const float *sums) {
-    const int t = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+    const int t = blockIdx.x / AB_SUM_CTAS, kvh = blockIdx.y, b = blockIdx.z;
     Entry e;
     if (!entry_of(p, b, e)) return;
     const int j0 = t * 128;
@@ -760,10 +763,11 @@ __global__ void __launch_bounds__(256) k_attn_sink_sum(const __grid_constant__ R
     if (pieces < 1) pieces = 1;
     const float *base = sums + sink_slot(cutting, p.Hkv, p.D, b, kvh, t, 0);
     const size_t step = (size_t)2 * 128 * p.D;
-    for (int i = threadIdx.x * 8; i < 2 * keys * p.D; i += 256 * 8) {
+    for (int i = (blockIdx.x % AB_SUM_CTAS * 256 + threadIdx.x) * 8; i < 2 * keys * p.D; i += AB_SUM_CTAS * 256 * 8) {
         const int which = i / (keys * p.D), at = i - which * keys * p.D;  // 0: dk, 1: dv
         const int r = at / p.D, d = at - r * p.D;
         float x[8] = {};
+#pragma unroll 4
         for (int k = 0; k < pieces; ++k) {
             float y[8];
             load8<false>(reinterpret_cast<const uint8_t *>(base + k * step + ((size_t)which * 128 + r) * p.D + d), y);

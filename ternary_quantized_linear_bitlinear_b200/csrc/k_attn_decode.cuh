@@ -49,7 +49,8 @@ struct DecodeAttnParams {
     float scale_log2;   // scale * log2(e)
     uint8_t *out;
     float *lse;
-    long long *cum;     // workspace: [B + 1] line places before sequence b's segments
+    long long *open;    // workspace: [CTAs][4] the segment a CTA begins but does not end: sequence (-1: none), first
+                        // query head, query heads, last CTA
     float *part;        // workspace: [2 * CTAs][gsize][DP + 2]
 };
 
@@ -79,12 +80,13 @@ __device__ __forceinline__ int entry_len(const DecodeAttnParams &p, int b, int *
     if (s < 0 || s >= p.kv.max_seqs) return 0;
     const int len = __ldg(p.kv.lengths + s);
     const int most = p.kv.max_pages << p.kv.ps_log;
+    if (len < 0 || len > most) raise_device_error(DEVERR_INDEX);
     return len < 0 ? 0 : len < most ? len : most;
 }
 
 // The line: segment `seg` of sequence b starts at cum[b] + seg * (count +
 // AD_OH); its first batch stands AD_OH places later.
-constexpr int AD_OH = 4;
+constexpr int AD_OH = 6;
 
 __device__ __forceinline__ float redux_max(float x) {
     float r;
@@ -626,8 +628,18 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::OCC) k_attn_decode(const __g
     if (threadIdx.x < 2 * WARPS) s_pb[threadIdx.x] = -1;
     C::init(s_bar);
     pdl_wait();
-    // places before each sequence (CTA 0 leaves them for the join), and the
-    // sequences in which the pieces of this CTA's warps begin
+    // the sequences in which the pieces of this CTA's warps begin
+    // an entry without a visible key (its sequence is empty, or a bad index says so), by the one thread that meets it
+    auto nothing_seen = [&](int b) {
+        const int seq = p.seq_ids != nullptr ? __ldg(p.seq_ids + b) : b;
+        if (seq < 0) return;  // padding
+        if (seq >= p.kv.max_seqs) {
+            raise_device_error(DEVERR_INDEX);
+            return;
+        }
+        for (int i = 0; i < p.Hq * p.D; ++i) put_out(p, (size_t)b * p.Hq + i / p.D, i % p.D, 0.f);
+        for (int h = 0; h < p.Hq; ++h) put_lse(p, (size_t)b * p.Hq + h, 0.f, 0.f);
+    };
     auto places = [&](int b) {  // of one segment of sequence b
         int seq, n = 0;
         if (b < p.B) n = visible_of<NB>(entry_len(p, b, &seq), p.window, p.sinks).count;
@@ -652,7 +664,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::OCC) k_attn_decode(const __g
         if (p.B <= T) total = (long long)sum * segs;
         const long long piece = (total + gw - 1) / gw;
         const long long here = at + (long long)pre * segs, next = here + (long long)n * segs;
-        if (blockIdx.x == 0 && b < p.B) p.cum[b] = here;
+        if (b < p.B && n == 0 && b % gridDim.x == blockIdx.x) nothing_seen(b);
         if (n > 0) {
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
@@ -665,7 +677,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::OCC) k_attn_decode(const __g
         }
         at += (long long)sum * segs;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.cum[p.B] = total;
+    if (threadIdx.x == 0) p.open[blockIdx.x * 4] = -1;
     __syncthreads();
     const long long piece = (total + gw - 1) / gw;
     const long long from = ((long long)blockIdx.x * WARPS + warp) * piece;
@@ -759,6 +771,12 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::OCC) k_attn_decode(const __g
                 a += c * row[d];
                 ll += c * row[DP + 1];
             }
+            if (i == 0 && c0 == (int)blockIdx.x && c1 > c0) {
+                p.open[blockIdx.x * 4 + 1] = h0;
+                p.open[blockIdx.x * 4 + 2] = gn;
+                p.open[blockIdx.x * 4 + 3] = c1;
+                p.open[blockIdx.x * 4] = pb;
+            }
             if (c0 == c1) {
                 const size_t row = (size_t)pb * p.Hq + h0 + g;
                 if (d < p.D) put_out(p, row, d, ll > 0.f ? a / ll : 0.f);
@@ -775,42 +793,17 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::OCC) k_attn_decode(const __g
     }
 }
 
-// Joins what spans CTAs, one CTA per (entry, query head); entries without a
-// visible key get out = 0, lse = -inf.
+// Joins what spans CTAs: CTA (c, g) the g-th query head of the segment that
+// CTA c of the launch before began and left open.
 template <int DP>
-__global__ void __launch_bounds__(AD_JOIN_THREADS) k_attn_join(const __grid_constant__ DecodeAttnParams p, int ctas,
-                                                               int warps) {
+__global__ void __launch_bounds__(AD_JOIN_THREADS) k_attn_join(const __grid_constant__ DecodeAttnParams p) {
     constexpr int ROW = DP + 2;
-    const int segs = p.Hkv * p.parts;
-    const int b = blockIdx.x, h = blockIdx.y;
-    const int kvh = h / p.group, part = (h - kvh * p.group) / p.gsize;
-    const int seg = kvh * p.parts + part, g = h - kvh * p.group - part * p.gsize;
+    const int c0 = blockIdx.x, g = blockIdx.y, d = threadIdx.x;
     pdl_wait();
-    const int seq = p.seq_ids != nullptr ? p.seq_ids[b] : b;
-    const long long cum = p.cum[b], next = p.cum[b + 1], total = p.cum[p.B];
-    if (seq < 0) return;
-    if (seq >= p.kv.max_seqs) {
-        if (threadIdx.x == 0 && h == 0) raise_device_error(DEVERR_INDEX);
-        return;
-    }
-    const size_t row = (size_t)b * p.Hq + h;
-    const int d = threadIdx.x;
-    if (h == 0 && d == 0) {
-        const int len = p.kv.lengths[seq];
-        if (len < 0 || len > (long long)p.kv.max_pages << p.kv.ps_log) raise_device_error(DEVERR_INDEX);
-    }
-    const long long width = (next - cum) / segs;
-    if (width == 0) {
-        if (d < p.D) put_out(p, row, d, 0.f);
-        if (d == 0) put_lse(p, row, 0.f, 0.f);
-        return;
-    }
-    const long long gw = (long long)ctas * warps;
-    const long long cta_piece = (total + gw - 1) / gw * warps;
-    const long long s0 = cum + seg * width + AD_OH, s1 = cum + (seg + 1) * width - 1;
-    const int c0 = (int)(s0 / cta_piece), c1 = (int)(s1 / cta_piece);
-    if (c0 == c1) return;  // finished by its CTA
-    const int n = c1 - c0 + 1;
+    const long long b = p.open[c0 * 4];
+    const int h0 = (int)p.open[c0 * 4 + 1], gn = (int)p.open[c0 * 4 + 2], n = (int)p.open[c0 * 4 + 3] - c0 + 1;
+    if (b < 0 || g >= gn) return;
+    const size_t row = (size_t)b * p.Hq + h0 + g;
     // CTA c0 holds the segment's beginning in its second slot, the others what follows in their first
     auto part_of = [&](int i) {
         return p.part + (((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.gsize + g) * ROW;
