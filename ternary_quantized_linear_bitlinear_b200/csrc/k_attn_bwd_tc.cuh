@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::BARS; ++i) mbar_init(bar0 + 8 * i, 1);
-        mbar_init(DSR, 256);
-        mbar_init(DSR + 8, 256);
+        mbar_init(DSR, 8);
+        mbar_init(DSR + 8, 8);
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (n > 0) {  // on their way while TMEM is allocated
@@ -337,9 +337,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                     pk[j] = pack_bf16(x, y);
                 }
                 tc_st16(s_col(u) + lane_at + 64 * c + 16 * q, pk);
-                tc_wait_st();
-                tc_before();
-                mbar_arrive(DSR + 8 * q);
+                tc_hand_over(DSR + 8 * q);
             }
         }
         if (ok && n > 0) ok = __all_sync(0xffffffffu, tc_wait(OUT, 0, TO, s_abort));
@@ -469,8 +467,8 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::BARS; ++i) mbar_init(bar0 + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(PR + 8 * i, 256);
-            mbar_init(DSR + 8 * i, 256);
+            mbar_init(PR + 8 * i, 8);
+            mbar_init(DSR + 8 * i, 8);
         }
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -662,9 +660,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
                 tc_st16(s_col + lane_at + 64 * c + 16 * q, pk);
-                tc_wait_st();
-                tc_before();
-                mbar_arrive(PR + 8 * q);
+                tc_hand_over(PR + 8 * q);
             }
             ok = __all_sync(0xffffffffu, tc_wait(DPF, (u32)(u & 1), TO, s_abort));
             if (!ok) break;
@@ -687,9 +683,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                     pk[j + 1] = pack_bf16(a, b2);
                 }
                 tc_st16(dp_col + lane_at + 64 * c + 16 * q, pk);
-                tc_wait_st();
-                tc_before();
-                mbar_arrive(DSR + 8 * q);
+                tc_hand_over(DSR + 8 * q);
             }
         }
         if (ok && n > 0) ok = __all_sync(0xffffffffu, tc_wait(OUT, 0, TO, s_abort));

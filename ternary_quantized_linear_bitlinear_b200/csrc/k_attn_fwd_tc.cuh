@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::BARS; ++i) mbar_init(bar0 + 8 * i, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(PF + 8 * i, 128);
+        for (int i = 0; i < 4; ++i) mbar_init(PF + 8 * i, 4);
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         // Q is on its way while TMEM is allocated
@@ -329,9 +329,7 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
                 }
                 tc_st16(s_col(half) + lane_at + 16 * c, pk);
                 if (c & 1) {
-                    tc_wait_st();
-                    tc_before();
-                    mbar_arrive(PF + 8 * (2 * half + (c >> 1)));
+                    tc_hand_over(PF + 8 * (2 * half + (c >> 1)));
                 }
             }
             float x0, x1, x2, x3;

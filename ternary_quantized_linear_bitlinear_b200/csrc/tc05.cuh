@@ -110,6 +110,15 @@ __device__ __forceinline__ void tc_gemm_nt(u32 d, u64 a, u64 b, u32 idesc) {
     }
 }
 
+// What the warp stored to TMEM is handed over: one arrival per warp (an arrival
+// per thread costs the barrier a few cycles each).
+__device__ __forceinline__ void tc_hand_over(u32 bar) {
+    tc_wait_st();
+    tc_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // 32 columns of this thread's TMEM lane (call tc_wait_ld before using them).
 __device__ __forceinline__ void tc_ld32(u32 *r, u32 addr) {
     asm volatile(
