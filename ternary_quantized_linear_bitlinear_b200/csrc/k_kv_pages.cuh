@@ -55,29 +55,45 @@ __device__ __forceinline__ int block_scan(int v, int *total, int *scratch) {
     return scratch[warp] + x - v;
 }
 
-// Free pages among the first `n` entries of refs.
-__device__ __forceinline__ long long count_free(const int *refs, int n, int *scratch) {
-    int c = 0;
-    for (int i = threadIdx.x; i < n; i += KV_THREADS) c += refs[i] == 0;
-    int total;
-    block_scan(c, &total, scratch);
-    return total;
-}
+// Pages lo .. hi - 1 that are free (or in use), in ascending order: every warp
+// takes a contiguous share of whole 32-page groups, counts its pages once,
+// and one scan over the warps gives each its first rank.  count() is a CTA-wide
+// call and returns the total; give(rank, page) then runs for each page of rank
+// < wanted.
+struct PagePick {
+    const int *refs;
+    int lo, hi, begin, end, first;
+    bool in_use;
 
-// Calls give(rank, page) for the free pages in ascending order, rank <
-// wanted.  The caller knows that there are enough of them.
-template <typename F>
-__device__ __forceinline__ void hand_out(const int *refs, int n, int wanted, int *scratch, F give) {
-    int base = 0;
-    for (int i0 = 0; i0 < n && base < wanted; i0 += KV_THREADS) {
-        const int i = i0 + threadIdx.x;
-        const int is = i < n && refs[i] == 0;
+    __device__ __forceinline__ bool is(int i) const { return i < hi && (refs[i] != 0) == in_use; }
+    __device__ __forceinline__ int count(const int *r, int lo_, int hi_, bool used, int *scratch) {
+        refs = r, lo = lo_, hi = hi_, in_use = used;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int share = (hi > lo ? (hi - lo + KV_THREADS - 1) / KV_THREADS : 0) * 32;
+        begin = lo + warp * share;
+        end = begin + share < hi ? begin + share : hi;
+        int c = 0;
+#pragma unroll 4
+        for (int i = begin + lane; i < end; i += 32) c += is(i) ? 1 : 0;
+        c = __reduce_add_sync(0xffffffffu, c);
         int total;
-        const int rank = base + block_scan(is, &total, scratch);
-        if (is && rank < wanted) give(rank, i);
-        base += total;
+        first = block_scan(lane == 0 ? c : 0, &total, scratch);
+        first = __shfl_sync(0xffffffffu, first, 0);
+        return total;
     }
-}
+    template <typename F>
+    __device__ __forceinline__ void each(int wanted, F give) const {
+        const int lane = threadIdx.x & 31;
+        int rank = first;
+        for (int i0 = begin; i0 < end && rank < wanted; i0 += 32) {
+            const bool mine = i0 + lane < end && is(i0 + lane);
+            const u32 all = __ballot_sync(0xffffffffu, mine);
+            const int r = rank + __popc(all & ((1u << lane) - 1u));
+            if (mine && r < wanted) give(r, i0 + lane);
+            rank += __popc(all);
+        }
+    }
+};
 
 // Shared memory of the planning kernels: 64 ints of scratch, one bit per
 // sequence (twice for a fork), then one int per entry (+ 1).
@@ -131,7 +147,8 @@ __global__ void __launch_bounds__(KV_THREADS) k_kv_extend(const __grid_constant_
         sum += total;
     }
     __syncthreads();
-    const long long free_pages = count_free(p.t.refs, p.t.num_pages, scratch);
+    PagePick pick;
+    const int free_pages = pick.count(p.t.refs, 0, p.t.num_pages, false, scratch);
     const int status = *bad ? *bad : sum > free_pages ? KV_NO_PAGES : KV_OK;
     if (threadIdx.x == 0) *p.status = status;
     if (p.active != nullptr)
@@ -140,7 +157,7 @@ __global__ void __launch_bounds__(KV_THREADS) k_kv_extend(const __grid_constant_
     const int want = (int)sum;
     if (threadIdx.x == 0) first[p.n] = want;
     __syncthreads();
-    hand_out(p.t.refs, p.t.num_pages, want, scratch, [&](int rank, int page) {
+    pick.each(want, [&](int rank, int page) {
         int lo = 0, hi = p.n - 1;  // the last entry with first <= rank
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -244,7 +261,9 @@ __global__ void __launch_bounds__(KV_THREADS) k_kv_fork_plan(const __grid_consta
         want += total;
     }
     __syncthreads();
-    const int status = *bad ? *bad : want > count_free(p.t.refs, p.t.num_pages, scratch) ? KV_NO_PAGES : KV_OK;
+    PagePick pick;
+    const int free_pages = pick.count(p.t.refs, 0, p.t.num_pages, false, scratch);
+    const int status = *bad ? *bad : want > free_pages ? KV_NO_PAGES : KV_OK;
     if (threadIdx.x == 0) {
         *p.status = status;
         p.plan[0] = status == KV_OK;
@@ -252,7 +271,7 @@ __global__ void __launch_bounds__(KV_THREADS) k_kv_fork_plan(const __grid_consta
     if (status != KV_OK) return;
     // the new pages by rank, behind the pairs; entries pick theirs up below
     int *pages = p.plan + 1 + 2 * p.n;
-    hand_out(p.t.refs, p.t.num_pages, want, scratch, [&](int rank, int page) {
+    pick.each(want, [&](int rank, int page) {
         pages[rank] = page;
         p.t.refs[page] = 1;
     });
@@ -337,20 +356,14 @@ struct KvCompactParams {
 __global__ void __launch_bounds__(KV_THREADS) k_kv_compact_plan(const __grid_constant__ KvCompactParams p) {
     __shared__ int scratch[64];
     const int n = p.t.num_pages;
-    const int live = n - (int)count_free(p.t.refs, n, scratch);
-    const int m = (int)count_free(p.t.refs, live, scratch);
+    PagePick holes, movers;
+    const int live = holes.count(p.t.refs, 0, n, true, scratch);
+    const int m = holes.count(p.t.refs, 0, live, false, scratch);
+    movers.count(p.t.refs, live, n, true, scratch);
     int *pair = p.plan + 2, *to = p.plan + 2 + 2 * (size_t)n;
-    hand_out(p.t.refs, live, m, scratch, [&](int rank, int page) { pair[2 * rank + 1] = page; });
-    int base = 0;
-    for (int i0 = live; i0 < n; i0 += KV_THREADS) {
-        const int i = i0 + threadIdx.x;
-        const int is = i < n && p.t.refs[i] != 0;
-        int total;
-        const int rank = base + block_scan(is, &total, scratch);
-        if (is) pair[2 * rank] = i;
-        else if (i < n) to[i] = i;
-        base += total;
-    }
+    holes.each(m, [&](int rank, int page) { pair[2 * rank + 1] = page; });
+    for (int i = live + threadIdx.x; i < n; i += KV_THREADS) to[i] = i;
+    movers.each(m, [&](int rank, int page) { pair[2 * rank] = page; });
     __syncthreads();
     for (int r = threadIdx.x; r < m; r += KV_THREADS) {
         const int a = pair[2 * r], b = pair[2 * r + 1];
