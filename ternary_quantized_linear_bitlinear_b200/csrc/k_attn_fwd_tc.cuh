@@ -50,16 +50,20 @@ struct RaggedMaps {
     CUtensorMap q, k, v, dout;
 };
 
-// Tiles of a CTA's halves: half h sees sink tiles below ns[h] and wt[h] .. last[h].
+// Which of a CTA's tiles (numbered as the CTA walks them) a half takes part in:
+// the first ns and lo .. hi.
 struct HalfTiles {
-    int ns, wt, last;  // last < 0: none
-    __device__ __forceinline__ bool has(int t) const { return last >= 0 && (t < ns || (t >= wt && t <= last)); }
+    int ns, lo, hi;
+    __device__ __forceinline__ bool has(int u) const { return u < ns || (u >= lo && u <= hi); }
+    __device__ __forceinline__ bool any() const { return hi >= 0; }
 };
-__device__ __forceinline__ HalfTiles half_tiles(const RaggedParams &p, int p0, int p1, int nk) {
+__device__ __forceinline__ HalfTiles half_tiles(const RaggedParams &p, const KeyTiles &all, int p0, int p1, int nk) {
     const KeyTiles t = key_tiles<AF_KEYS>(p, p0, p1, nk);
-    HalfTiles h{t.ns, t.wt, -1};
-    if (t.count > 0) h.last = t.wt + t.count - t.ns - 1;
-    return h;
+    if (t.count == 0) return HalfTiles{0, 0, -1};
+    const int by = all.ns - all.wt;  // number of tile t among the CTA's: t + by from all.wt on
+    // (a half that starts above the CTA's first window tile may count sink tiles of its own among those)
+    const int ns = t.ns <= all.ns ? t.ns : t.ns >= all.wt ? t.ns + by : all.ns;
+    return HalfTiles{ns, t.wt + by, t.wt + t.count - t.ns - 1 + by};
 }
 
 template <int DP>
@@ -92,11 +96,9 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
     const int rows0 = e.nq - i0 < 128 ? e.nq - i0 : 128;
     const int rows1 = e.nq - i0 <= 128 ? 0 : e.nq - i0 - 128 < 128 ? e.nq - i0 - 128 : 128;
     const int pos0 = i0 + e.off;
-    HalfTiles ht[2];
-    ht[0] = half_tiles(p, pos0, pos0 + rows0 - 1, e.nk);
-    ht[1] = HalfTiles{0, 0, -1};
-    if (rows1 > 0) ht[1] = half_tiles(p, pos0 + 128, pos0 + 128 + rows1 - 1, e.nk);
     const KeyTiles all = key_tiles<AF_KEYS>(p, pos0, pos0 + rows0 + rows1 - 1, e.nk);
+    const HalfTiles ht0 = half_tiles(p, all, pos0, pos0 + rows0 - 1, e.nk);
+    const HalfTiles ht1 = rows1 > 0 ? half_tiles(p, all, pos0 + 128, pos0 + 128 + rows1 - 1, e.nk) : HalfTiles{0, 0, -1};
     const int count = all.count;
     auto tile_of = [&](int u) { return u < all.ns ? u : all.wt + (u - all.ns); };
 
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         // Q is on its way while TMEM is allocated
         for (int half = 0; half < 2; ++half) {
-            if (ht[half].last < 0) continue;
+            if (!(half ? ht1 : ht0).any()) continue;
             mbar_arrive_expect_tx(QF + 8 * half, F::TILE);
             tc_load_rows<DP>(&maps.q, sbase + half * F::TILE, h, e.q0 + i0 + 128 * half, QF + 8 * half);
         }
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
                 }
                 // what was requested lands before the CTA exits
                 for (int half = 0; half < 2; ++half)
-                    if (ht[half].last >= 0) tc_wait(QF + 8 * half, 0, TO, nullptr);
+                    if ((half ? ht1 : ht0).any()) tc_wait(QF + 8 * half, 0, TO, nullptr);
                 for (int j = ks - ST > 0 ? ks - ST : 0; j < ks; ++j)
                     tc_wait(KF + 8 * (j % ST), (u32)((j / ST) & 1), TO, nullptr);
                 for (int j = u - ST > 0 ? u - ST : 0; j < u; ++j) tc_wait(v_full(j), v_phase(j), TO, nullptr);
@@ -167,62 +169,57 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
             if (count > 0) {
                 constexpr u32 ID_QK = tc_idesc(AF_KEYS, false, false), ID_PV = tc_idesc(DP, false, true);
                 const bool leader = tc_elect();
-                bool ok = true;
-                int n[2] = {0, 0};  // tiles of a half whose P was consumed
-                int k_seen = -1, v_seen = -1;
                 const u64 q_desc = tc_desc_k(sbase), k_desc = tc_desc_k(sbase + F::OFF_K), v_desc = tc_desc_mn(sbase + F::OFF_V);
-                auto qk = [&](int half, int u) {
-                    const int s = u % ST;
-                    if (k_seen < u) {
-                        ok = ok && TC_WAIT_ALL(KF + 8 * s, (u32)((u / ST) & 1), TO, s_abort);
-                        k_seen = u;
-                    }
-                    if (n[half] == 0) ok = ok && TC_WAIT_ALL(QF + 8 * half, 0, TO, s_abort);
-                    if (!ok) return;
-                    tc_after();
+                bool ok = true;
+                int n0 = 0, n1 = 0;  // tiles of a half whose P was consumed
+                for (int half = 0; half < 2; ++half)
+                    if ((half ? ht1 : ht0).any()) ok = ok && TC_WAIT_ALL(QF + 8 * half, 0, TO, s_abort);
+                auto qk = [&](int half, int s) {
                     if (leader) {
                         tc_gemm_nt<DP>(s_col(half), q_desc + (u64)(half * F::TILE >> 4), k_desc + (u64)(s * F::TILE >> 4), ID_QK);
                         tc_commit(SF + 8 * half);
                     }
                     __syncwarp();
                 };
-                for (int half = 0; half < 2 && ok; ++half)
-                    if (ht[half].has(tile_of(0))) qk(half, 0);
-                if (ok && leader) tc_commit(KE);
-                for (int u = 0; u < count && ok; ++u) {
-                    const int s = u % ST, t = tile_of(u);
-    #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (ok && ht[half].has(t)) {
-                            if (v_seen < u) {
-                                ok = TC_WAIT_ALL(t == cut_tile ? FIX : VF + 8 * s, v_phase(u), TO, s_abort);
-                                v_seen = u;
-                            }
-                            const u64 v = v_desc + (u64)(s * F::TILE >> 4);
-                            // the weights of the first 64 keys are ready before the others
-    #pragma unroll
-                            for (int part = 0; part < 2; ++part) {
-                                ok = ok && TC_WAIT_ALL(PF + 8 * (2 * half + part), (u32)(n[half] & 1), TO, s_abort);
-                                if (!ok) break;
-                                tc_after();
-                                if (leader) {
-    #pragma unroll
-                                    for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
-                                        tc_mma_ts(o_col(half), s_col(half) + 8 * kk, v + (u64)(kk * 2048 >> 4), ID_PV,
-                                                  n[half] != 0 || kk != 0);
-                                }
-                                __syncwarp();
-                            }
-                            if (!ok) break;
-                            ++n[half];
-                            if (t == ht[half].last && leader) tc_commit(OF + 8 * half);
+                auto pv = [&](int half, int &n, int s, bool last) {
+                    const u64 v = v_desc + (u64)(s * F::TILE >> 4);
+                    // the weights of the first 64 keys are ready before the others
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        ok = ok && TC_WAIT_ALL(PF + 8 * (2 * half + part), (u32)(n & 1), TO, s_abort);
+                        if (!ok) return;
+                        tc_after();
+                        if (leader) {
+#pragma unroll
+                            for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
+                                tc_mma_ts(o_col(half), s_col(half) + 8 * kk, v + (u64)(kk * 2048 >> 4), ID_PV, n != 0 || kk != 0);
                         }
-                        if (ok && u + 1 < count && ht[half].has(tile_of(u + 1))) qk(half, u + 1);
+                        __syncwarp();
                     }
+                    ++n;
+                    if (last && leader) tc_commit(OF + 8 * half);
+                };
+                ok = ok && TC_WAIT_ALL(KF, 0, TO, s_abort);
+                if (ok) {
+                    tc_after();
+                    if (ht0.has(0)) qk(0, 0);
+                    if (ht1.has(0)) qk(1, 0);
+                    if (leader) tc_commit(KE);
+                }
+                for (int u = 0; u < count && ok; ++u) {
+                    const int s = u % ST, s1 = (u + 1) % ST;
+                    const bool more = u + 1 < count;
+                    ok = TC_WAIT_ALL(cuts && !more ? FIX : VF + 8 * s, v_phase(u), TO, s_abort);
+                    if (more) ok = ok && TC_WAIT_ALL(KF + 8 * s1, (u32)(((u + 1) / ST) & 1), TO, s_abort);
+                    if (!ok) break;
+                    if (ht0.has(u)) pv(0, n0, s, u == ht0.hi);
+                    if (ok && more && ht0.has(u + 1)) qk(0, s1);
+                    if (ok && ht1.has(u)) pv(1, n1, s, u == ht1.hi);
+                    if (ok && more && ht1.has(u + 1)) qk(1, s1);
                     if (!ok) break;
                     if (leader) {
                         tc_commit(VE + 8 * s);
-                        if (u + 1 < count) tc_commit(KE + 8 * ((u + 1) % ST));
+                        if (more) tc_commit(KE + 8 * s1);
                     }
                     __syncwarp();
                 }
@@ -252,7 +249,7 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
         const int row = i0 + 128 * half + r, rows = half ? rows1 : rows0;
         const int pos = row + e.off;
         const u32 lane_at = (u32)((warp & 3) * 32) << 16;
-        const HalfTiles mine = ht[half];
+        const HalfTiles mine = half ? ht1 : ht0;
         const int first_pos = pos0 + 128 * half, last_pos = first_pos + rows - 1;
         const float sl = p.scale_log2;
         float m = -INFINITY, l = 0.f;
@@ -260,7 +257,7 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
         bool ok = true;
         for (int u = 0; u < count; ++u) {
             const int t = tile_of(u);
-            if (!mine.has(t)) continue;
+            if (!mine.has(u)) continue;
             ok = __all_sync(0xffffffffu, tc_wait(SF + 8 * half, (u32)(n & 1), TO, s_abort));
             if (!ok) break;
             tc_after();
