@@ -461,8 +461,17 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     const bool to_sums = t < cutting.sink_tiles;
     const int qt = t_hi - t_lo + 1 > 0 ? t_hi - t_lo + 1 : 0, n = qt * p.group;
     if (far && n == 0) return;  // (its sums are not read)
-    auto head_of = [&](int u) { return kvh * p.group + u / qt; };
-    auto row_of = [&](int u) { return (t_lo + u % qt) * 128; };
+    // the walk: query tiles t_lo .. t_hi of the group's first head, then of the next
+    struct Walk {
+        int head, tile;
+    };
+    auto advance = [&](Walk &w) {
+        if (++w.tile > t_hi) {
+            w.tile = t_lo;
+            ++w.head;
+        }
+    };
+    const Walk start{kvh * p.group, t_lo};
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::BARS; ++i) mbar_init(bar0 + 8 * i, 1);
@@ -489,8 +498,9 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
         if (lane == 0 && n > 0) {
             bool ok = true;
             int u = 0;
-            for (; u < n; ++u) {
-                const int s = u % ST, row = e.q0 + row_of(u), h = head_of(u);
+            Walk at = start;
+            for (; u < n; ++u, advance(at)) {
+                const int s = u % ST, row = e.q0 + at.tile * 128, h = at.head;
                 if (u >= ST && !tc_wait(QE + 8 * s, (u32)((u / ST) & 1) ^ 1, TO, s_abort)) {
                     ok = false;
                     break;
@@ -585,11 +595,12 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     } else if (warp == 2) {
         // lse and delta of a query tile; rows behind the last query are cleared and get weights of zero
         bool ok = true;
-        for (int u = 0; u < n; ++u) {
-            const int s = u % ST, i0 = row_of(u);
+        Walk at = start;
+        for (int u = 0; u < n; ++u, advance(at)) {
+            const int s = u % ST, i0 = at.tile * 128;
             const int rows = e.nq - i0 < 128 ? e.nq - i0 : 128;
             float lse[4], delta[4];
-            const size_t stat = (size_t)head_of(u) * p.Tq + e.q0 + i0;
+            const size_t stat = (size_t)at.head * p.Tq + e.q0 + i0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int r = lane + 32 * k;
@@ -621,8 +632,9 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
         const u32 lane_at = (u32)((warp & 3) * 32) << 16;
         const f32x2 sl2 = pack2(p.scale_log2, p.scale_log2);
         bool ok = true;
-        for (int u = 0; u < n; ++u) {
-            const int s = u % ST, i0 = row_of(u);
+        Walk walk = start;
+        for (int u = 0; u < n; ++u, advance(walk)) {
+            const int s = u % ST, i0 = walk.tile * 128;
             ok = __all_sync(0xffffffffu, tc_wait(LF + 8 * s, (u32)((u / ST) & 1), TO, s_abort) &&
                                              tc_wait(SF, (u32)(u & 1), TO, s_abort));
             if (!ok) break;
