@@ -70,7 +70,9 @@ typedef struct {
 /* them NULL: not written.  cache NULL: no pages are written; otherwise      */
 /* k and v go to their position's page (cache->lengths is used for the       */
 /* positions; `lengths` must then be NULL).  q may be NULL with q_out NULL,  */
-/* k and v may both be NULL with k_out, v_out and cache NULL.                */
+/* k and v may both be NULL with k_out, v_out and cache NULL.  An output may */
+/* be the input it comes from (same type, contiguous), not overlap it        */
+/* otherwise; with a cache a sequence is listed once per call.               */
 /* ------------------------------------------------------------------------ */
 bl_status bl_rope_append(const void *q, const void *k, const void *v, bl_dtype xdt, int64_t q_stride,
                          int64_t k_stride, int64_t v_stride, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
@@ -161,7 +163,7 @@ bl_status bl_kv_compact(void *pool, int64_t planes, int64_t page_bytes, int32_t 
 /*   dv = P^T do;  dS = P o (do v^T - rowsum(do o o));                       */
 /*   dq = scale dS k;  dk = scale dS^T q                                     */
 /* dk and dv sum over the query heads of a shared head.  P and dS are        */
-/* rounded to bfloat16 (half a step, 2^-9 relative, per term) where they     */
+/* rounded to bfloat16 (half a step, 2^-8 relative, per term) where they     */
 /* enter the tensor cores; everything else is float32 until the outputs are  */
 /* rounded once.  No atomics: the same inputs give the same bits.            */
 /*                                                                           */

@@ -640,6 +640,15 @@ def _rows3(t, name: str, cur: int, heads: int | None = None, D: int | None = Non
     return stride
 
 
+def _on(stream, fn, *args):
+    """fn(*args) with `stream` current: what the call allocates then belongs to
+    the stream it is used on (memory of another stream's pool may still be in
+    use there, or be handed out again before this call's kernels have run)."""
+    _stream(stream)  # of the current device?
+    with torch.cuda.stream(stream):
+        return fn(*args)
+
+
 def _buf(t, name: str, dtype, min_numel: int, cur: int):
     if not (_ok(t, dtype, cur) and t.numel() >= min_numel):
         _dev(t, name, dtype, min_numel)
@@ -712,6 +721,9 @@ def bl_rope_append(q=None, k=None, v=None, rope=None, cu_seqlens=None, lengths=N
     at 0, 1, ...  inverse=True rotates back (the gradient).  An output may be
     the very tensor it comes from (same dtype, same rows), not overlap it
     otherwise."""
+    if stream is not None:
+        return _on(stream, bl_rope_append, q, k, v, rope, cu_seqlens, lengths, seq_ids, k_pages, v_pages, tables, out_dtype,
+                   q_out, k_out, v_out, keep_kv, inverse)
     cur = _current_device()
     first = q if q is not None else k
     if first is None:
@@ -777,7 +789,7 @@ def bl_rope_append(q=None, k=None, v=None, rope=None, cu_seqlens=None, lengths=N
     rc = lib().bl_rope_append(_ptr(q), _ptr(k), _ptr(v), _DTYPES[dt], qs, ks, vs, T, Hq, Hkv, D, _ptr(rope),
                               0 if rope is None else rope.shape[0], int(inverse), _ptr(cu_seqlens), B, _ptr(seq_ids),
                               None if cache is not None else _ptr(lengths), max_seqs, cache, _ptr(q_out), _ptr(k_out),
-                              _ptr(v_out), _DTYPES[odt], _stream(stream))
+                              _ptr(v_out), _DTYPES[odt], _stream(None))
     if rc:
         _check(rc, "bl_rope_append")
     return q_out, k_out, v_out
@@ -795,6 +807,9 @@ def bl_attn_decode(q, k_pages, v_pages, tables, lengths, seq_ids=None, window: i
     otherwise the last `window` and the first `sinks`; scale defaults to
     D ** -0.5.  Calls that may run at the same time need workspaces of their
     own (the default: a new one per call)."""
+    if stream is not None:
+        return _on(stream, bl_attn_decode, q, k_pages, v_pages, tables, lengths, seq_ids, window, sinks, scale, out, lse,
+                   return_lse, workspace)
     cur = _current_device()
     qs = _rows3(q, "q", cur)
     B, Hq, D = q.shape
@@ -818,7 +833,7 @@ def bl_attn_decode(q, k_pages, v_pages, tables, lengths, seq_ids=None, window: i
         _buf(workspace, "workspace", torch.uint8, 1, cur)
     rc = L.bl_attn_decode(q.data_ptr(), _DTYPES[q.dtype], qs, B, Hq, Hkv, D, cache, _ptr(seq_ids), window, sinks,
                           D ** -0.5 if scale is None else scale, workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size(), out.data_ptr(), _ptr(lse), _stream(stream))
+                          workspace.numel() * workspace.element_size(), out.data_ptr(), _ptr(lse), _stream(None))
     if rc:
         _check(rc, "bl_attn_decode")
     return (out, lse) if return_lse else out
@@ -836,6 +851,8 @@ def bl_kv_extend(tables, lengths, refs, seq_ids, counts, page_size: int, status=
     ones, lengths raised -> status int32 [1] (0: done; otherwise nothing was
     changed, see bitlinear_attn.h).  active int32 [n], when given, becomes
     seq_ids, or -1 throughout when the call failed."""
+    if stream is not None:
+        return _on(stream, bl_kv_extend, tables, lengths, refs, seq_ids, counts, page_size, status, active)
     cur = _current_device()
     max_seqs, max_pages = _tables2(tables, lengths, refs, cur)
     ids = _buf(seq_ids, "seq_ids", torch.int32, 1, cur)
@@ -845,7 +862,7 @@ def bl_kv_extend(tables, lengths, refs, seq_ids, counts, page_size: int, status=
     if active is not None:
         _i32(active, "active", n, cur)
     rc = lib().bl_kv_extend(tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(), refs.numel(), page_size, max_seqs,
-                            max_pages, ids, cnt, n, status.data_ptr(), _ptr(active), _stream(stream))
+                            max_pages, ids, cnt, n, status.data_ptr(), _ptr(active), _stream(None))
     if rc:
         _check(rc, "bl_kv_extend")
     return status
@@ -853,11 +870,13 @@ def bl_kv_extend(tables, lengths, refs, seq_ids, counts, page_size: int, status=
 
 def bl_kv_free(tables, lengths, refs, seq_ids, page_size: int, stream=None):
     """The sequences end: their pages' refs fall by one, rows become -1, lengths 0."""
+    if stream is not None:
+        return _on(stream, bl_kv_free, tables, lengths, refs, seq_ids, page_size)
     cur = _current_device()
     max_seqs, max_pages = _tables2(tables, lengths, refs, cur)
     ids = _buf(seq_ids, "seq_ids", torch.int32, 1, cur)
     rc = lib().bl_kv_free(tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(), refs.numel(), page_size, max_seqs,
-                          max_pages, ids, seq_ids.numel(), _stream(stream))
+                          max_pages, ids, seq_ids.numel(), _stream(None))
     if rc:
         _check(rc, "bl_kv_free")
 
@@ -879,6 +898,8 @@ def bl_kv_fork(pool, tables, lengths, refs, src, dst, status=None, workspace=Non
     """Sequence dst[i] (empty) becomes a copy of src[i]: full pages are shared, a
     last partial page is copied in every plane of pool [..., num_pages, Hkv,
     page_size, D] -> status int32 [1], as for bl_kv_extend."""
+    if stream is not None:
+        return _on(stream, bl_kv_fork, pool, tables, lengths, refs, src, dst, status, workspace)
     cur = _current_device()
     max_seqs, max_pages = _tables2(tables, lengths, refs, cur)
     planes, page_bytes, ps = _pool(pool, refs, cur)
@@ -893,7 +914,7 @@ def bl_kv_fork(pool, tables, lengths, refs, src, dst, status=None, workspace=Non
         _buf(workspace, "workspace", torch.uint8, 1, cur)
     rc = L.bl_kv_fork(pool.data_ptr(), planes, page_bytes, tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(),
                       refs.numel(), ps, max_seqs, max_pages, a, b, n, workspace.data_ptr(),
-                      workspace.numel() * workspace.element_size(), status.data_ptr(), _stream(stream))
+                      workspace.numel() * workspace.element_size(), status.data_ptr(), _stream(None))
     if rc:
         _check(rc, "bl_kv_fork")
     return status
@@ -902,6 +923,8 @@ def bl_kv_fork(pool, tables, lengths, refs, src, dst, status=None, workspace=Non
 def bl_kv_compact(pool, tables, refs, n_live=None, workspace=None, stream=None):
     """The pages in use move to the lowest numbers, in every plane of pool;
     tables and refs follow -> n_live int32 [1], the pages in use."""
+    if stream is not None:
+        return _on(stream, bl_kv_compact, pool, tables, refs, n_live, workspace)
     cur = _current_device()
     max_seqs, max_pages = _tables2(tables, None, refs, cur)
     planes, page_bytes, _ = _pool(pool, refs, cur)
@@ -917,7 +940,7 @@ def bl_kv_compact(pool, tables, refs, n_live=None, workspace=None, stream=None):
         _buf(workspace, "workspace", torch.uint8, 1, cur)
     rc = L.bl_kv_compact(pool.data_ptr(), planes, page_bytes, tables.data_ptr(), refs.data_ptr(), pages, max_seqs,
                          max_pages, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                         n_live.data_ptr(), _stream(stream))
+                         n_live.data_ptr(), _stream(None))
     if rc:
         _check(rc, "bl_kv_compact")
     return n_live
@@ -942,6 +965,8 @@ def bl_attn_forward(q, k, v, cu_q, cu_k, max_q: int, max_k: int, window: int = 0
     keys cu_k[b] .. cu_k[b+1] - 1, the last query standing at the last key.
     window = 0 sees every earlier key, otherwise the last `window` and the
     first `sinks` -> (o bfloat16 [Tq, Hq, D], lse float32 [Hq, Tq])."""
+    if stream is not None:
+        return _on(stream, bl_attn_forward, q, k, v, cu_q, cu_k, max_q, max_k, window, sinks, scale, o, lse)
     cur = _current_device()
     strides, (Tq, Tk, Hq, Hkv, D), (a, b, B) = _ragged(q, k, v, cu_q, cu_k, cur)
     if o is None:
@@ -954,7 +979,7 @@ def bl_attn_forward(q, k, v, cu_q, cu_k, max_q: int, max_k: int, window: int = 0
         _buf(lse, "lse", torch.float32, Hq * Tq, cur)
     rc = lib().bl_attn_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, Tq, Tk, Hq, Hkv, D, a, b, B, max_q,
                                max_k, window, sinks, D ** -0.5 if scale is None else scale, o.data_ptr(),
-                               lse.data_ptr(), _stream(stream))
+                               lse.data_ptr(), _stream(None))
     if rc:
         _check(rc, "bl_attn_forward")
     return o, lse
@@ -965,6 +990,9 @@ def bl_attn_backward(do, q, k, v, o, lse, cu_q, cu_k, max_q: int, max_k: int, wi
     """Gradients of bl_attn_forward (o, lse its outputs; do bfloat16 [Tq, Hq, D])
     -> (dq [Tq, Hq, D], dk, dv [Tk, Hkv, D]) bfloat16; dk and dv sum over the
     query heads that share a head."""
+    if stream is not None:
+        return _on(stream, bl_attn_backward, do, q, k, v, o, lse, cu_q, cu_k, max_q, max_k, window, sinks, scale, dq, dk, dv,
+                   workspace)
     cur = _current_device()
     b16 = torch.bfloat16
     strides, (Tq, Tk, Hq, Hkv, D), (a, b, B) = _ragged(q, k, v, cu_q, cu_k, cur)
@@ -992,7 +1020,7 @@ def bl_attn_backward(do, q, k, v, o, lse, cu_q, cu_k, max_q: int, max_k: int, wi
     rc = L.bl_attn_backward(do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dos,
                             *strides, Tq, Tk, Hq, Hkv, D, a, b, B, max_q, max_k, window, sinks,
                             D ** -0.5 if scale is None else scale, workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _stream(stream))
+                            workspace.numel() * workspace.element_size(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _stream(None))
     if rc:
         _check(rc, "bl_attn_backward")
     return dq, dk, dv

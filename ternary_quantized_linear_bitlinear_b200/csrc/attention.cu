@@ -436,6 +436,10 @@ bl_status bl_kv_compact(void *pool, int64_t planes, int64_t page_bytes, int32_t 
 // ---------------------------------------------------------------------------
 // ragged attention
 
+// A window or sinks beyond every length mean no window, or every key.
+static int norm_window(int64_t w) { return (int)(w > (1 << 25) ? 0 : w); }
+static int norm_sinks(int64_t s) { return (int)(s > (1 << 25) ? (1 << 25) : s); }
+
 static bl_status ragged_params(RaggedParams *P, const void *q, const void *k, const void *v, int64_t q_stride,
                                int64_t k_stride, int64_t v_stride, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv,
                                int64_t D, const int32_t *cu_q, const int32_t *cu_k, int64_t B, int64_t max_q,
@@ -469,9 +473,8 @@ static bl_status ragged_params(RaggedParams *P, const void *q, const void *k, co
     P->B = (int)B;
     P->max_q = (int)max_q;
     P->max_k = (int)max_k;
-    // beyond every length they mean the same
-    P->window = (int)(window > (1 << 25) ? 0 : window);
-    P->sinks = (int)(sinks > (1 << 25) ? (1 << 25) : sinks);
+    P->window = norm_window(window);
+    P->sinks = norm_sinks(sinks);
     P->scale = scale;
     P->scale_log2 = scale * LOG2E;
     return BL_OK;
@@ -506,7 +509,8 @@ size_t bl_attn_backward_workspace_bytes(int64_t Tq, int64_t Tk, int64_t Hq, int6
                                         int64_t max_q, int64_t max_k, int64_t window, int64_t sinks) {
     if (Tq < 1 || Tk < 1 || B < 1 || max_q < 1 || max_k < 1 || window < 0 || sinks < 0 || check_heads(Hq, Hkv, D) != BL_OK)
         return 0;
-    const DkvCut cut = dkv_cut(max_q, max_k, window, sinks);
+    if (max_q >= (1 << 24) || max_k >= (1 << 24) || B > 65535) return 0;
+    const DkvCut cut = dkv_cut(max_q, max_k, norm_window(window), norm_sinks(sinks));
     return align256((size_t)Tq * Hq * 4) + sink_slot(cut, (int)Hkv, (int)D, (int)B, 0, 0, 0) * 4;
 }
 

@@ -368,8 +368,8 @@ struct DecodeFma {
 // terms that stand in the rows of the same product, so that nothing is
 // rounded below 32 bits:
 //   DEC_BF16  bfloat16 q, up to 8 heads: q is one term (rows 0 - 7); the
-//             weights p two (rows 0 - 7 and 8 - 15: 16 bits, 2^-17 relative
-//             beside the output's 2^-9 rounding)
+//             weights p two (rows 0 - 7 and 8 - 15: 2^-16 relative beside the
+//             output's half step of 2^-8)
 //   DEC_F32_4 float32 q, up to 4 heads: q and p three terms each (24 bits) in
 //             rows g, g + 8 and g + 4
 //   DEC_F32_8 float32 q, up to 8 heads: rows g and g + 8, and the third
@@ -611,8 +611,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::OCC) k_attn_decode(const __g
     static_assert(C::G * ROW * 4 <= RING, "a partial fits a ring");
     extern __shared__ __align__(128) uint8_t s_ring[];
     __shared__ __align__(8) u64 s_bar[C::BARS];
-    __shared__ int scratch[64];
-    __shared__ long long s_before[WARPS];
+    __shared__ long long scratch[33], s_before[WARPS];
     __shared__ int s_b[WARPS];
     __shared__ int s_pb[2 * WARPS], s_pseg[2 * WARPS];      // whose partial (sequence, segment), -1: none
     __shared__ long long s_p0[2 * WARPS], s_p1[2 * WARPS];  // line places of that segment's first and last batch
@@ -649,9 +648,9 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::OCC) k_attn_decode(const __g
     long long at = 0;
     if (p.B > T) {
         for (int b0 = 0; b0 < p.B; b0 += T) {
-            int sum;
-            block_scan(b0 == 0 ? mine : places(b0 + threadIdx.x), &sum, scratch);
-            at += (long long)sum * segs;
+            long long sum;  // (lengths up to 2^31: 64 bits)
+            block_scan<long long>(b0 == 0 ? mine : places(b0 + threadIdx.x), &sum, scratch);
+            at += sum * segs;
         }
     }
     long long total = at;
@@ -659,11 +658,11 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::OCC) k_attn_decode(const __g
     for (int b0 = 0; b0 < p.B; b0 += T) {
         const int b = b0 + threadIdx.x;
         const int n = b0 == 0 ? mine : places(b);
-        int sum;
-        const int pre = block_scan(n, &sum, scratch);
-        if (p.B <= T) total = (long long)sum * segs;
+        long long sum;
+        const long long pre = block_scan<long long>(n, &sum, scratch);
+        if (p.B <= T) total = sum * segs;
         const long long piece = (total + gw - 1) / gw;
-        const long long here = at + (long long)pre * segs, next = here + (long long)n * segs;
+        const long long here = at + pre * segs, next = here + (long long)n * segs;
         if (b < p.B && n == 0 && b % gridDim.x == blockIdx.x) nothing_seen(b);
         if (n > 0) {
 #pragma unroll
@@ -675,7 +674,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::OCC) k_attn_decode(const __g
                 }
             }
         }
-        at += (long long)sum * segs;
+        at += sum * segs;
     }
     if (threadIdx.x == 0) p.open[blockIdx.x * 4] = -1;
     __syncthreads();
@@ -691,7 +690,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, C::OCC) k_attn_decode(const __g
     }
 
     C core(s_ring + (size_t)warp * RING, s_bar);
-    while (at < end) {
+    while (at < end && b < p.B) {
         // the segment at `at`
         int seq;
         Segment sg;

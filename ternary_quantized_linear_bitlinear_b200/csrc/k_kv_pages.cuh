@@ -26,25 +26,26 @@ struct KvTables {
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Exclusive prefix sum of one int per thread over the CTA; *total the sum.
-// scratch: 33 ints of shared memory, reused by the next call.
-__device__ __forceinline__ int block_scan(int v, int *total, int *scratch) {
+// Exclusive prefix sum of one value per thread over the CTA; *total the sum.
+// scratch: 33 values of shared memory, reused by the next call.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T *total, T *scratch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    int x = v;
+    T x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     __syncthreads();  // the previous call's readers are done
     if (lane == 31) scratch[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        const int w = lane < nw ? scratch[lane] : 0;
-        int s = w;
+        const T w = lane < nw ? scratch[lane] : 0;
+        T s = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            const T y = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += y;
         }
         if (lane < nw) scratch[lane] = s - w;
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(KV_THREADS) k_kv_fork_plan(const __grid_consta
         const int len = p.t.lengths[a], full = len >> p.t.ps_log;
         if (first[i] >= 0) {
             const int page = pages[first[i]];
-            p.plan[1 + 2 * i] = p.t.tables[(size_t)a * p.t.max_pages + full];
+            const int old = p.t.tables[(size_t)a * p.t.max_pages + full];
+            p.plan[1 + 2 * i] = old < 0 ? -2 : old;  // (-2: the table names no page; the copy reports it)
             p.plan[2 + 2 * i] = page;
             p.t.tables[(size_t)b * p.t.max_pages + full] = page;
         }

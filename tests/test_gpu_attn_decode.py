@@ -203,3 +203,24 @@ def test_offsets_beyond_32_bits():
     x = torch.randn(1, Hkv, D, generator=g).cuda()
     api.bl_rope_append(k=x, v=x, lengths=lengths, k_pages=kp, v_pages=vp, tables=tables)
     assert torch.equal(kp[ids[4], :, 299 % ps], x[0].bfloat16())
+
+
+def test_given_stream_and_large_values_of_everything():
+    kp, vp, tables, lengths, ks, vs = _cache([300, 70], 16, 2, 64, torch.bfloat16, 18)
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(19)).cuda()
+    ref = api.bl_attn_decode(q, kp, vp, tables, lengths)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = [api.bl_attn_decode(q, kp, vp, tables, lengths, window=w, sinks=s, stream=side)
+            for w, s in ((0, 0), (1 << 40, 0), (0, 1 << 40), (300, 1 << 50), (1, 1 << 40))]
+    torch.cuda.synchronize()
+    for o in outs[:4]:
+        assert torch.equal(o, ref)
+    _check(outs[4], torch.zeros(2, 4), q, ks, vs, [], 0, 0, 0.125)
+    assert (outs[4] - ref).abs().max() < 1e-5       # every key is a sink: the same keys, perhaps in other batches
+    # lengths no table can hold, for many entries: cut off and reported
+    huge = torch.full((2,), 2 ** 31 - 1, dtype=torch.int32).cuda()
+    api.bl_attn_decode(q.repeat(300, 1, 1), kp, vp, tables, huge, torch.zeros(600, dtype=torch.int32).cuda())
+    with pytest.raises(api.BitLinearError) as e:
+        api.bl_check_device_error()
+    assert e.value.status == 9

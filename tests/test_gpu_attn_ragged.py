@@ -174,3 +174,48 @@ def test_capture_of_a_training_step():
     g.replay()
     torch.cuda.synchronize()
     _compare([150, 60], [150, 60], 4, 2, 64, 64, 2, 64 ** -0.5, q, k, v, do, o, lse, grads)
+
+
+def test_window_and_sinks_beyond_every_length():
+    q, k, v, do, (cq, ck) = _inputs([300, 40], [300, 40], 4, 2, 64, 26)
+    o, lse = api.bl_attn_forward(q, k, v, cq, ck, 300, 300)
+    g = api.bl_attn_backward(do, q, k, v, o, lse, cq, ck, 300, 300)
+    for window, sinks in ((1 << 40, 0), (1 << 40, 1 << 50), (301, 0)):
+        o2, lse2 = api.bl_attn_forward(q, k, v, cq, ck, 300, 300, window, sinks)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        g2 = api.bl_attn_backward(do, q, k, v, o, lse, cq, ck, 300, 300, window, sinks)
+        assert all(torch.equal(a, b) for a, b in zip(g, g2))
+    # a window with every key a sink hides nothing
+    o2, lse2 = api.bl_attn_forward(q, k, v, cq, ck, 300, 300, 7, 1 << 40)
+    g2 = api.bl_attn_backward(do, q, k, v, o2, lse2, cq, ck, 300, 300, 7, 1 << 40)
+    _compare([300, 40], [300, 40], 4, 2, 64, 0, 0, 64 ** -0.5, q, k, v, do, o2, lse2, g2)
+
+
+def test_long_sequence():
+    """Many tiles, several waves of CTAs, sinks cut into pieces."""
+    n = 2500
+    q, k, v, do, (cq, ck) = _inputs([n], [n], 2, 1, 128, 27)
+    for window, sinks in ((0, 0), (200, 5)):
+        o, lse = api.bl_attn_forward(q, k, v, cq, ck, n, n, window, sinks)
+        g = api.bl_attn_backward(do, q, k, v, o, lse, cq, ck, n, n, window, sinks)
+        api.bl_check_device_error()
+        _compare([n], [n], 2, 1, 128, window, sinks, 128 ** -0.5, q, k, v, do, o, lse, g)
+
+
+def test_given_stream():
+    """A call on a stream that is not the current one allocates there too: right whatever the current stream's pool
+    hands out meanwhile."""
+    q, k, v, do, (cq, ck) = _inputs([500, 300], [500, 300], 4, 2, 64, 28)
+    o, lse = api.bl_attn_forward(q, k, v, cq, ck, 500, 500, 100, 3)
+    g = api.bl_attn_backward(do, q, k, v, o, lse, cq, ck, 500, 500, 100, 3)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    results = []
+    for _ in range(6):
+        o2, lse2 = api.bl_attn_forward(q, k, v, cq, ck, 500, 500, 100, 3, stream=side)
+        results.append((o2, lse2, *api.bl_attn_backward(do, q, k, v, o2, lse2, cq, ck, 500, 500, 100, 3, stream=side)))
+        junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(4)]
+        del junk
+    torch.cuda.synchronize()
+    for r in results:
+        assert all(torch.equal(a, b) for a, b in zip(r, (o, lse, *g)))

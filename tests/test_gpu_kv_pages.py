@@ -163,3 +163,43 @@ def test_captured_steps():
         torch.cuda.synchronize()
         assert ref() == (st[0, 0].item(), st[1, 0].item())
         model.check(kv.tables, kv.lengths, kv.refs)
+
+
+def test_a_table_that_names_no_page_is_reported():
+    kv, _ = _pair(8, 8, 4, 4)
+    kv.extend(_i32([0]), _i32([12]))
+    kv.tables[0, 1] = -1
+    assert kv.fork(_i32([0]), _i32([1])).item() == 0
+    with pytest.raises(api.BitLinearError) as e:
+        api.bl_check_device_error()
+    assert e.value.status == 9
+    kv.tables[0, 0] = 10 ** 6
+    kv.fork(_i32([0]), _i32([2]))
+    with pytest.raises(api.BitLinearError):
+        api.bl_check_device_error()
+    kv.free(_i32([0]))
+    with pytest.raises(api.BitLinearError):
+        api.bl_check_device_error()
+
+
+def test_given_stream():
+    kv, model = _pair(64, 8, 8, 8)
+    side = torch.cuda.Stream()
+    ids, counts = _i32([0, 3]), _i32([20, 9])
+    torch.cuda.synchronize()
+    data = kv.pool.clone()
+    torch.cuda.synchronize()
+    st = [kv.extend(ids, counts, stream=side), kv.fork(ids, _i32([1, 2]), stream=side)]
+    kv.free(_i32([0]), stream=side)
+    n = kv.compact(stream=side)
+    torch.cuda.synchronize()
+    model.extend([0, 3], [20, 9])
+    model.fork([0, 3], [1, 2])
+    for a, b in model.moves:
+        data[:, :, b] = data[:, :, a]
+    model.free([0])
+    assert n.item() == model.compact() and [s.item() for s in st] == [0, 0]
+    for a, b in model.moves:
+        data[:, :, b] = data[:, :, a]
+    model.check(kv.tables, kv.lengths, kv.refs)
+    assert torch.equal(kv.pool, data)
