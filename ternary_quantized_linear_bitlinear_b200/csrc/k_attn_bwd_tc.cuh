@@ -46,7 +46,7 @@ constexpr unsigned long long AB_TIMEOUT_NS = 2000000000ull;
 
 template <int DP>
 struct DqShape {
-    static constexpr int KS = 3, VS = 2;  // stages of K (read twice, two steps apart) and V
+    static constexpr int KS = 3, VS = DP == 64 ? 3 : 2;  // stages of K (read twice, two steps apart) and V
     static constexpr int TILE = DP / 64 * TC_BLOCK;
     static constexpr int OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE, OFF_D = OFF_V + VS * TILE;
     static constexpr int OFF_BAR = OFF_D + 2 * 128 * 4;
@@ -156,19 +156,17 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             bool ok = TC_WAIT_ALL(QF, 0, TO, s_abort);
             const u64 q_desc = tc_desc_k(sbase), do_desc = tc_desc_k(sbase + F::OFF_DO), k_desc = tc_desc_k(sbase + F::OFF_K),
                       v_desc = tc_desc_k(sbase + F::OFF_V), kt_desc = tc_desc_mn(sbase + F::OFF_K);
-            auto form_s = [&](int u) {
-                ok = ok && TC_WAIT_ALL(k_full(u), k_phase(u), TO, s_abort);
-                if (!ok) return;
+            auto k_ready = [&](int u) { ok = ok && TC_WAIT_ALL(k_full(u), k_phase(u), TO, s_abort); };
+            auto v_ready = [&](int u) { ok = ok && TC_WAIT_ALL(v_full(u), v_phase(u), TO, s_abort); };
+            auto form_s = [&](int u, int ks) {
                 tc_after();
                 if (leader) {
-                    tc_gemm_nt<DP>(s_col(u), q_desc, k_desc + (u64)(u % KS * F::TILE >> 4), ID_S);
+                    tc_gemm_nt<DP>(s_col(u), q_desc, k_desc + (u64)(ks * F::TILE >> 4), ID_S);
                     tc_commit(SF + 8 * (u & 1));
                 }
                 __syncwarp();
             };
             auto form_dp = [&](int u) {
-                ok = ok && TC_WAIT_ALL(v_full(u), v_phase(u), TO, s_abort);
-                if (!ok) return;
                 tc_after();
                 if (leader) {
                     tc_gemm_nt<DP>(dp_col, do_desc, v_desc + (u64)(u % VS * F::TILE >> 4), ID_S);
@@ -177,11 +175,16 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 }
                 __syncwarp();
             };
-            form_s(0);
-            form_dp(0);
-            if (n > 1) form_s(1);
+            k_ready(0);
+            if (ok) form_s(0, 0);
+            v_ready(0);
+            if (ok) form_dp(0);
+            if (n > 1) k_ready(1);
+            if (ok && n > 1) form_s(1, 1);
+            int ks = 0;  // u % KS
             for (int u = 0; u < n && ok; ++u) {
-                const u64 k = kt_desc + (u64)(u % KS * F::TILE >> 4);
+                const u64 k = kt_desc + (u64)(ks * F::TILE >> 4);
+                const int ks2 = ks == 0 ? 2 : ks - 1;  // (u + 2) % KS
                 // columns 0 - 63 of dS are at the buffer's start, 64 - 127 at its column 64; the first half of each is
                 // ready first (part 0: steps 0, 1, 4, 5)
                 auto add = [&](int part) {
@@ -192,7 +195,10 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                                   u != 0 || part != 0 || i != 0);
                     }
                 };
-                ok = TC_WAIT_ALL(DSR, (u32)(u & 1), TO, s_abort);
+                // (the next V has landed long before the weights of this tile are ready; the K after the next is only
+                // asked for when the last step's dQ is done)
+                if (u + 1 < n) v_ready(u + 1);
+                ok = ok && TC_WAIT_ALL(DSR, (u32)(u & 1), TO, s_abort);
                 if (!ok) break;
                 tc_after();
                 if (leader) add(0);
@@ -204,10 +210,14 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 if (u + 1 < n) form_dp(u + 1);
                 if (leader) {
                     add(1);
-                    tc_commit(KE + 8 * (u % KS));
+                    tc_commit(KE + 8 * ks);
                 }
                 __syncwarp();
-                if (u + 2 < n) form_s(u + 2);
+                if (u + 2 < n) {
+                    k_ready(u + 2);
+                    if (ok) form_s(u + 2, ks2);
+                }
+                ks = ks == KS - 1 ? 0 : ks + 1;
             }
             if (!ok && lane == 0) {
                 raise_device_error(DEVERR_TIMEOUT_MMA);
@@ -375,7 +385,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
 
 template <int DP>
 struct DkvShape {
-    static constexpr int ST = 2;
+    static constexpr int ST = DP == 64 ? 4 : 2;
     static constexpr int TILE = DP / 64 * TC_BLOCK;
     static constexpr int OFF_V = TILE, OFF_Q = 2 * TILE, OFF_DO = OFF_Q + ST * TILE, OFF_L = OFF_DO + ST * TILE;
     static constexpr int OFF_BAR = OFF_L + ST * 2 * 128 * 4;
@@ -559,10 +569,12 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             }
             __syncwarp();
             for (int u = 0; u < n && ok; ++u) {
+                // with more than two stages the next query tile has landed long before this one's weights are ready
+                if (ST > 2 && u + 1 < n) q_ready(u + 1);
                 add_when(PR, u, dv_col, s_col, dot_desc + stage(u));
                 if (!ok) break;
                 if (u + 1 < n) {
-                    q_ready(u + 1);
+                    if (ST == 2) q_ready(u + 1);
                     if (!ok) break;
                     if (leader) {
                         tc_gemm_nt<DP>(s_col, k_desc, q_desc + stage(u + 1), ID_S);
