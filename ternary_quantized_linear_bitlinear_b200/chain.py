@@ -126,6 +126,8 @@ class DecodeChain:
                              f"{c.tables.shape[1] * c.page_size}")
 
     def launches_per_step(self) -> int:
+        """Kernel launches of a step (with a cache: at most; an attention small
+        enough for one CTA needs no join)."""
         return 5 * len(self.layers) if self.cache is None else 8 * len(self.layers) + 1
 
     def _attend(self, li: int, b, stream):
