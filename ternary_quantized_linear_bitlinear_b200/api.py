@@ -10,6 +10,7 @@ the library's kernels; if the library is missing, loading fails loudly.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import struct
@@ -123,6 +124,13 @@ _SIGS = {
 EXPORTED = tuple(_SIGS)
 
 
+# attn_binding.so, once loaded, and what bind() there takes.
+_FAST = None
+_FAST_ENTRIES = ("bl_rope_append", "bl_attn_decode_workspace_bytes", "bl_attn_decode", "bl_kv_extend", "bl_kv_free",
+                 "bl_kv_fork_workspace_bytes", "bl_kv_fork", "bl_kv_compact_workspace_bytes", "bl_kv_compact",
+                 "bl_attn_forward", "bl_attn_backward_workspace_bytes", "bl_attn_backward")
+
+
 def lib_path() -> str:
     return _build.LIB
 
@@ -140,8 +148,22 @@ def lib():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
+        _load_binding(L)
         _LIB = L
     return _LIB
+
+
+def _load_binding(L):
+    """attn_binding.so, the compiled way to the attention calls, with the addresses of L's entry points."""
+    global _FAST
+    path = _build.BINDING
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with `python -m ternary_quantized_linear_bitlinear_b200.build`")
+    spec = importlib.util.spec_from_file_location("attn_binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(tuple(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _FAST_ENTRIES))
+    _FAST = module
 
 
 def status_string(status: int) -> str:
@@ -589,9 +611,10 @@ def bl_linear_grouped(Ws, X, subln_gain=None, subln_eps: float = 1e-6, Ys=None, 
 
 # -- attention and its cache (include/bitlinear_attn.h) ------------------------
 #
-# These calls are a few microseconds of GPU work at decode sizes, so a valid
-# buffer is recognised by one expression (_ok, _ok3) and only a doubtful one
-# goes through the checks that say what is wrong with it.
+# These calls are a few microseconds of GPU work at decode sizes, so the plain
+# valid call is recognised and made by compiled code (_FAST,
+# csrc/attn_binding.cpp).  What it does not take comes back as None and goes
+# through the checks here.
 
 _Tensor = torch.Tensor
 _B16 = torch.bfloat16
@@ -647,6 +670,13 @@ def _on(stream, fn, *args):
     _stream(stream)  # of the current device?
     with torch.cuda.stream(stream):
         return fn(*args)
+
+
+def _answer(done, where: str):
+    """What _FAST returned: the results, or the status of a call that was refused."""
+    if done.__class__ is int:
+        _check(done, where)
+    return done
 
 
 def _buf(t, name: str, dtype, min_numel: int, cur: int):
@@ -724,6 +754,11 @@ def bl_rope_append(q=None, k=None, v=None, rope=None, cu_seqlens=None, lengths=N
     if stream is not None:
         return _on(stream, bl_rope_append, q, k, v, rope, cu_seqlens, lengths, seq_ids, k_pages, v_pages, tables, out_dtype,
                    q_out, k_out, v_out, keep_kv, inverse)
+    if _FAST is not None:
+        done = _FAST.rope_append(q, k, v, rope, cu_seqlens, lengths, seq_ids, k_pages, v_pages, tables, out_dtype, q_out,
+                                 k_out, v_out, keep_kv, inverse)
+        if done is not None:
+            return _answer(done, "bl_rope_append")
     cur = _current_device()
     first = q if q is not None else k
     if first is None:
@@ -810,6 +845,11 @@ def bl_attn_decode(q, k_pages, v_pages, tables, lengths, seq_ids=None, window: i
     if stream is not None:
         return _on(stream, bl_attn_decode, q, k_pages, v_pages, tables, lengths, seq_ids, window, sinks, scale, out, lse,
                    return_lse, workspace)
+    if _FAST is not None:
+        done = _FAST.attn_decode(q, k_pages, v_pages, tables, lengths, seq_ids, window, sinks, scale, out, lse,
+                                 return_lse, workspace)
+        if done is not None:
+            return _answer(done, "bl_attn_decode")
     cur = _current_device()
     qs = _rows3(q, "q", cur)
     B, Hq, D = q.shape
@@ -853,6 +893,10 @@ def bl_kv_extend(tables, lengths, refs, seq_ids, counts, page_size: int, status=
     seq_ids, or -1 throughout when the call failed."""
     if stream is not None:
         return _on(stream, bl_kv_extend, tables, lengths, refs, seq_ids, counts, page_size, status, active)
+    if _FAST is not None:
+        done = _FAST.kv_extend(tables, lengths, refs, seq_ids, counts, page_size, status, active)
+        if done is not None:
+            return _answer(done, "bl_kv_extend")
     cur = _current_device()
     max_seqs, max_pages = _tables2(tables, lengths, refs, cur)
     ids = _buf(seq_ids, "seq_ids", torch.int32, 1, cur)
@@ -872,6 +916,10 @@ def bl_kv_free(tables, lengths, refs, seq_ids, page_size: int, stream=None):
     """The sequences end: their pages' refs fall by one, rows become -1, lengths 0."""
     if stream is not None:
         return _on(stream, bl_kv_free, tables, lengths, refs, seq_ids, page_size)
+    if _FAST is not None:
+        done = _FAST.kv_free(tables, lengths, refs, seq_ids, page_size)
+        if done is not None:
+            return None if done == 0 else _answer(done, "bl_kv_free")
     cur = _current_device()
     max_seqs, max_pages = _tables2(tables, lengths, refs, cur)
     ids = _buf(seq_ids, "seq_ids", torch.int32, 1, cur)
@@ -900,6 +948,10 @@ def bl_kv_fork(pool, tables, lengths, refs, src, dst, status=None, workspace=Non
     page_size, D] -> status int32 [1], as for bl_kv_extend."""
     if stream is not None:
         return _on(stream, bl_kv_fork, pool, tables, lengths, refs, src, dst, status, workspace)
+    if _FAST is not None:
+        done = _FAST.kv_fork(pool, tables, lengths, refs, src, dst, status, workspace)
+        if done is not None:
+            return _answer(done, "bl_kv_fork")
     cur = _current_device()
     max_seqs, max_pages = _tables2(tables, lengths, refs, cur)
     planes, page_bytes, ps = _pool(pool, refs, cur)
@@ -925,6 +977,10 @@ def bl_kv_compact(pool, tables, refs, n_live=None, workspace=None, stream=None):
     tables and refs follow -> n_live int32 [1], the pages in use."""
     if stream is not None:
         return _on(stream, bl_kv_compact, pool, tables, refs, n_live, workspace)
+    if _FAST is not None:
+        done = _FAST.kv_compact(pool, tables, refs, n_live, workspace)
+        if done is not None:
+            return _answer(done, "bl_kv_compact")
     cur = _current_device()
     max_seqs, max_pages = _tables2(tables, None, refs, cur)
     planes, page_bytes, _ = _pool(pool, refs, cur)
@@ -967,6 +1023,10 @@ def bl_attn_forward(q, k, v, cu_q, cu_k, max_q: int, max_k: int, window: int = 0
     first `sinks` -> (o bfloat16 [Tq, Hq, D], lse float32 [Hq, Tq])."""
     if stream is not None:
         return _on(stream, bl_attn_forward, q, k, v, cu_q, cu_k, max_q, max_k, window, sinks, scale, o, lse)
+    if _FAST is not None:
+        done = _FAST.attn_forward(q, k, v, cu_q, cu_k, max_q, max_k, window, sinks, scale, o, lse)
+        if done is not None:
+            return _answer(done, "bl_attn_forward")
     cur = _current_device()
     strides, (Tq, Tk, Hq, Hkv, D), (a, b, B) = _ragged(q, k, v, cu_q, cu_k, cur)
     if o is None:
@@ -993,6 +1053,11 @@ def bl_attn_backward(do, q, k, v, o, lse, cu_q, cu_k, max_q: int, max_k: int, wi
     if stream is not None:
         return _on(stream, bl_attn_backward, do, q, k, v, o, lse, cu_q, cu_k, max_q, max_k, window, sinks, scale, dq, dk, dv,
                    workspace)
+    if _FAST is not None:
+        done = _FAST.attn_backward(do, q, k, v, o, lse, cu_q, cu_k, max_q, max_k, window, sinks, scale, dq, dk, dv,
+                                   workspace)
+        if done is not None:
+            return _answer(done, "bl_attn_backward")
     cur = _current_device()
     b16 = torch.bfloat16
     strides, (Tq, Tk, Hq, Hkv, D), (a, b, B) = _ragged(q, k, v, cu_q, cu_k, cur)
