@@ -8,10 +8,18 @@
 //
 // k_attn_dq_tc.  A CTA owns 128 queries of one head (TMEM lanes).  S and dP of
 // a key tile come from two products; dS goes back to TMEM as bf16 over S and
-// is the A operand of dQ += dS K.  S is double buffered: while the softmax
-// threads turn S(j), dP(j) into dS(j) the tensor core forms dQ(j - 1), dP(j)
-// and S(j + 1).  delta = rowsum(dO o O) starts the kernel; on the way it sums
-// P dP, the same quantity without O's bf16 rounding, which dK uses.
+// is the A operand of dQ += dS K.  The kernel starts from delta0 = rowsum(dO o
+// O) with the O that the forward rounded to bf16, and on the way sums delta =
+// rowsum(P o dP), the same quantity without that rounding, which dK uses.
+// delta0's error is common to a row, so dQ would be off by it times sum_j P_j
+// k_j, which keys with a mean do not average out (K and V of mean 4: a third of
+// dQ).  So R += P K is formed as well, P as bf16 beside dS over S, and
+//   dQ = scale (sum_j dS_j k_j + (delta0 - delta) R)
+// at the end: R's own rounding only weighs on the small difference.
+// TMEM is full: at D <= 64 S is double buffered (S(j + 1) is formed while the
+// softmax threads work on S(j)); at D > 64 two buffers serve S and dP in turn,
+// S(j + 1) taking the place of dP(j), and R(j) runs while the threads form
+// dS(j).
 //
 // k_attn_dkdv_tc.  A CTA owns 128 keys of one kv head (TMEM lanes) and walks
 // the query tiles that see them, for every query head that shares them, so dK
@@ -25,7 +33,7 @@
 // beyond the window's reach are cut into pieces of their own, whose float32
 // sums go to the workspace and are added in order by k_attn_sink_sum.
 //
-// Bound: seven products of 512 tensor cycles per pair of 128-tiles at D = 128
+// Bound: eight products of 512 tensor cycles per pair of 128-tiles at D = 128
 // against 2 x 1024 cycles of exponentials.
 //
 // Threads: warp 0 TMA producer, 1 TMEM allocator and MMA issuer, 2 rows'
@@ -50,7 +58,8 @@ struct DqShape {
     static constexpr int TILE = DP / 64 * TC_BLOCK;
     static constexpr int OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE, OFF_D = OFF_V + VS * TILE;
     static constexpr int OFF_BAR = OFF_D + 2 * 128 * 4;
-    static constexpr int BARS = 1 + 2 * KS + 2 * VS + 9;
+    static constexpr int BARS = 1 + 2 * KS + 2 * VS + 11;
+    static constexpr bool AHEAD = DP == 64;  // S(j + 1) has a buffer of its own
     static constexpr int SMEM = OFF_BAR + BARS * 8 + 16 + 1024;
 };
 static_assert(DqShape<128>::SMEM <= 227 * 1024, "dQ shared memory");
@@ -64,7 +73,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(af_raw) + 1023) & ~(uintptr_t)1023);
     const u32 sbase = smem_u32(sm), bar0 = sbase + F::OFF_BAR;
     const u32 QF = bar0, KF = bar0 + 8, KE = KF + 8 * KS, VF = KE + 8 * KS, VE = VF + 8 * VS, SF = VE + 8 * VS,
-              DPF = SF + 16, DSR = DPF + 8, OUT = DSR + 16, CUT = OUT + 8, FIX = CUT + 8, DRAIN = FIX + 8;
+              DPF = SF + 16, PR = DPF + 8, DSR = PR + 16, OUT = DSR + 16, CUT = OUT + 8, FIX = CUT + 8, DRAIN = FIX + 8;
     float *s_delta = reinterpret_cast<float *>(sm + F::OFF_D);  // [2][128]
     u32 *s_tmem = reinterpret_cast<u32 *>(sm + F::OFF_BAR + F::BARS * 8);
     volatile int *s_abort = reinterpret_cast<volatile int *>(sm + F::OFF_BAR + F::BARS * 8 + 4);
@@ -99,8 +108,10 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::BARS; ++i) mbar_init(bar0 + 8 * i, 1);
-        mbar_init(DSR, 8);
-        mbar_init(DSR + 8, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(PR + 8 * i, 8);
+            mbar_init(DSR + 8 * i, 8);
+        }
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (n > 0) {  // on their way while TMEM is allocated
@@ -115,7 +126,8 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     tc_after();
     const u32 tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
     auto s_col = [&](int j) { return tmem + 128u * (j & 1); };
-    const u32 dp_col = tmem + 256, dq_col = tmem + 384;
+    auto dp_col = [&](int j) { return F::AHEAD ? tmem + 256u : tmem + 128u * (~j & 1); };
+    const u32 dq_col = tmem + (F::AHEAD ? 384 : 256), r_col = dq_col + DP;
 
     if (warp == 0) {
         if (lane == 0 && n > 0) {
@@ -169,7 +181,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             auto form_dp = [&](int u) {
                 tc_after();
                 if (leader) {
-                    tc_gemm_nt<DP>(dp_col, do_desc, v_desc + (u64)(u % VS * F::TILE >> 4), ID_S);
+                    tc_gemm_nt<DP>(dp_col(u), do_desc, v_desc + (u64)(u % VS * F::TILE >> 4), ID_S);
                     tc_commit(DPF);
                     tc_commit(VE + 8 * (u % VS));
                 }
@@ -179,12 +191,12 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             if (ok) form_s(0, 0);
             v_ready(0);
             if (ok) form_dp(0);
-            if (n > 1) k_ready(1);
-            if (ok && n > 1) form_s(1, 1);
+            if (F::AHEAD && n > 1) k_ready(1);
+            if (F::AHEAD && ok && n > 1) form_s(1, 1);
             int ks = 0;  // u % KS
             for (int u = 0; u < n && ok; ++u) {
                 const u64 k = kt_desc + (u64)(ks * F::TILE >> 4);
-                const int ks2 = ks == 0 ? 2 : ks - 1;  // (u + 2) % KS
+                const int ks1 = ks == KS - 1 ? 0 : ks + 1, ks2 = ks == 0 ? 2 : ks - 1;  // (u + 1) % KS, (u + 2) % KS
                 // columns 0 - 63 of dS are at the buffer's start, 64 - 127 at its column 64; the first half of each is
                 // ready first (part 0: steps 0, 1, 4, 5)
                 auto add = [&](int part) {
@@ -195,10 +207,21 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                                   u != 0 || part != 0 || i != 0);
                     }
                 };
-                // (the next V has landed long before the weights of this tile are ready; the K after the next is only
-                // asked for when the last step's dQ is done)
+                // (the next V, and at D > 64 the next K, have landed long before the weights of this tile are ready; the
+                // K after the next is only asked for when the last step's dQ is done)
                 if (u + 1 < n) v_ready(u + 1);
-                ok = ok && TC_WAIT_ALL(DSR, (u32)(u & 1), TO, s_abort);
+                if (!F::AHEAD && u + 1 < n) k_ready(u + 1);
+                ok = ok && TC_WAIT_ALL(PR + 8 * (u & 1), (u32)((u >> 1) & 1), TO, s_abort);
+                if (!ok) break;
+                tc_after();
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        tc_mma_ts(r_col, s_col(u) + (kk / 4) * 64 + 32 + (kk % 4) * 8, k + (u64)(kk * 2048 >> 4), ID_Q,
+                                  u != 0 || kk != 0);
+                }
+                __syncwarp();
+                ok = TC_WAIT_ALL(DSR, (u32)(u & 1), TO, s_abort);
                 if (!ok) break;
                 tc_after();
                 if (leader) add(0);
@@ -206,14 +229,19 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 ok = TC_WAIT_ALL(DSR + 8, (u32)(u & 1), TO, s_abort);
                 if (!ok) break;
                 tc_after();
-                // dP first: the threads wait for it next
-                if (u + 1 < n) form_dp(u + 1);
+                // first what the threads wait for next: dP, or where it takes dP's place S (every thread has read dP)
+                if (u + 1 < n) {
+                    if (F::AHEAD) form_dp(u + 1);
+                    else form_s(u + 1, ks1);
+                }
                 if (leader) {
                     add(1);
                     tc_commit(KE + 8 * ks);
                 }
                 __syncwarp();
-                if (u + 2 < n) {
+                // (dP takes the place of P and dS, which the products before it have read)
+                if (!F::AHEAD && u + 1 < n) form_dp(u + 1);
+                if (F::AHEAD && u + 2 < n) {
                     k_ready(u + 2);
                     if (ok) form_s(u + 2, ks2);
                 }
@@ -277,7 +305,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             }
         }
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        float delta = s_delta[r];
+        const float delta0 = s_delta[r];
         // (a row that sees nothing has lse = -inf and only hidden keys)
         const float lse = r < rows ? p.lse[stat] * 1.44269504088896f : 0.f;
         const f32x2 sl2 = pack2(sl, sl), nlse2 = pack2(-lse, -lse);
@@ -285,7 +313,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
         bool ok = true;
         for (int u = 0; u < n; ++u) {
             ok = __all_sync(0xffffffffu, tc_wait(SF + 8 * (u & 1), (u32)((u >> 1) & 1), TO, s_abort));
-            if (!ok && n > 1) break;
+            if (!ok) break;
             tc_after();
             u32 w[64];
             tc_ld32(w, s_col(u) + lane_at + 64 * c);
@@ -310,32 +338,23 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 for (int j = 0; j < 64; ++j)
                     if (j > hi || (j < lo && j >= sk)) w[j] = 0u;
             }
-            ok = ok && __all_sync(0xffffffffu, tc_wait(DPF, (u32)(u & 1), TO, s_abort));
-            if (n == 1) {
-                // one tile holds all the row sees: delta without O's rounding, which weighs most on rows of few
-                // keys (the two halves of the columns meet at the barrier whatever the waits said)
-                tc_after();
-                float part = 0.f;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    u32 g[32];
-                    tc_ld32(g, dp_col + lane_at + 64 * c + 32 * q);
-                    tc_wait_ld();
+            for (int q = 0; q < 2; ++q) {
+                u32 pk[16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) part = fmaf(__uint_as_float(w[32 * q + j]), __uint_as_float(g[j]), part);
-                }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                s_delta[c * 128 + r] = part;
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                delta = s_delta[r] + s_delta[128 + r];
+                for (int j = 0; j < 16; ++j)
+                    pk[j] = pack_bf16(__uint_as_float(w[32 * q + 2 * j]), __uint_as_float(w[32 * q + 2 * j + 1]));
+                tc_st16(s_col(u) + lane_at + 64 * c + 32 + 16 * q, pk);
             }
+            tc_hand_over(PR + 8 * (u & 1));
+            ok = __all_sync(0xffffffffu, tc_wait(DPF, (u32)(u & 1), TO, s_abort));
             if (!ok) break;
             tc_after();
-            const f32x2 nd2 = pack2(-delta, -delta);
+            const f32x2 nd2 = pack2(-delta0, -delta0);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 u32 g[32], pk[16];
-                tc_ld32(g, dp_col + lane_at + 64 * c + 32 * q);
+                tc_ld32(g, dp_col(u) + lane_at + 64 * c + 32 * q);
                 tc_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -350,6 +369,13 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 tc_hand_over(DSR + 8 * q);
             }
         }
+        // delta, over both halves of the columns (the barriers are met whatever the waits said)
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        float sum, sum_hi;
+        unpack2(sum2, sum, sum_hi);
+        s_delta[c * 128 + r] = sum + sum_hi;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float delta = s_delta[r] + s_delta[128 + r];
         if (ok && n > 0) ok = __all_sync(0xffffffffu, tc_wait(OUT, 0, TO, s_abort));
         if (!ok) {
             if (lane == 0) {
@@ -358,19 +384,13 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             }
         } else {
             tc_after();
+            if (c == 0 && r < rows) delta_out[stat] = delta;
             // (the Q tile is not read any more)
             const int first = 32 * (warp & 3);
             tc_store_rows<DP / 2>(dq_col + lane_at + DP / 2 * c, n == 0, p.scale, sm + (warp - 4) * 32 * DP,
                                   p.dq + ((size_t)(e.q0 + i0 + first) * p.Hq + h) * p.D + DP / 2 * c,
-                                  (long long)p.Hq * p.D, rows - first, p.D - DP / 2 * c);
+                                  (long long)p.Hq * p.D, rows - first, p.D - DP / 2 * c, DP, delta0 - delta);
         }
-        // the row's sum of P dP over both halves of the columns (the barriers are met whatever the waits said)
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        float sum, sum_hi;
-        unpack2(sum2, sum, sum_hi);
-        s_delta[c * 128 + r] = sum + sum_hi;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (ok && c == 0 && r < rows) delta_out[stat] = s_delta[r] + s_delta[128 + r];
     }
     tc_before();
     __syncthreads();

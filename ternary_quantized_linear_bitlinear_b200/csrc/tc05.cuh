@@ -170,13 +170,14 @@ __device__ __forceinline__ void tc_load_rows(const CUtensorMap *map, u32 dst, in
 }
 
 // A warp's 32 TMEM lanes x COLS columns (from column address `col`, lanes
-// included), times f, as bf16 to rows of global memory: through the warp's own
+// included), plus g times those `beside` columns further on (0: none), times f,
+// as bf16 to rows of global memory: through the warp's own
 // 32 x COLS x 2 bytes of shared memory (16-byte chunks permuted by the row), so
 // that a row is written by neighbouring lanes.  Lane i's row goes to
 // out + i * stride, columns below `cols`, if i < rows.  empty: zeros instead.
 template <int COLS>
 __device__ __forceinline__ void tc_store_rows(u32 col, bool empty, float f, uint8_t *stage, uint16_t *out, long long stride,
-                                              int rows, int cols) {
+                                              int rows, int cols, int beside = 0, float g = 0.f) {
     constexpr int CH = COLS / 8, SWZ = CH < 8 ? CH - 1 : 7;
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -188,6 +189,13 @@ __device__ __forceinline__ void tc_store_rows(u32 col, bool empty, float f, uint
         } else {
             tc_ld32(o, col + 32 * k);
             tc_wait_ld();
+            if (beside != 0) {
+                u32 x[32];
+                tc_ld32(x, col + beside + 32 * k);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(fmaf(g, __uint_as_float(x[j]), __uint_as_float(o[j])));
+            }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
