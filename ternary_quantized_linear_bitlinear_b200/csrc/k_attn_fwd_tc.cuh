@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(AF_THREADS, 1)
 #pragma unroll
             for (int j = 8; j < 128; ++j) mq[j & 7] = fmaxf(mq[j & 7], __uint_as_float(w[j]));
             const float mx = fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])), fmaxf(fmaxf(mq[4], mq[5]), fmaxf(mq[6], mq[7])));
-            if (__any_sync(0xffffffffu, (mx - m) * sl > 8.f || m == -INFINITY)) {
+            // (rows behind the last query have no vote: they are another entry's, whose bits must not decide this one's)
+            if (__any_sync(0xffffffffu, r < rows && ((mx - m) * sl > 8.f || m == -INFINITY))) {
                 const float top = fmaxf(m, mx), c = m == -INFINITY ? 0.f : exp2_fast((m - top) * sl);
                 m = top;
                 l *= c;
