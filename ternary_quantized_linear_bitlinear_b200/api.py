@@ -14,6 +14,7 @@ import importlib.util
 import math
 import os
 import struct
+import warnings
 
 import torch
 
@@ -154,16 +155,25 @@ def lib():
 
 
 def _load_binding(L):
-    """attn_binding.so, the compiled way to the attention calls, with the addresses of L's entry points."""
+    """attn_binding.so, the compiled way to the attention calls, with the
+    addresses of L's entry points.  Only a shorter way: where it was not built
+    (no host compiler, no torch headers) or was built for another torch, the
+    attention calls go through the checks of this file, 5 to 10 us slower, and
+    nothing else changes."""
     global _FAST
     path = _build.BINDING
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with `python -m ternary_quantized_linear_bitlinear_b200.build`")
-    spec = importlib.util.spec_from_file_location("attn_binding", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    module.bind(tuple(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _FAST_ENTRIES))
-    _FAST = module
+    try:
+        spec = importlib.util.spec_from_file_location("attn_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        if module.torch_version != torch.__version__:
+            raise ImportError(f"built for torch {module.torch_version}, this is {torch.__version__}")
+        module.bind(tuple(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _FAST_ENTRIES))
+        _FAST = module
+    except (ImportError, OSError) as e:
+        _FAST = None
+        warnings.warn(f"{path}: {e}; attention calls take 5 to 10 us longer on the host (build it with "
+                      "`python -m ternary_quantized_linear_bitlinear_b200.build`)", RuntimeWarning, stacklevel=3)
 
 
 def status_string(status: int) -> str:

@@ -559,4 +559,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "attn_binding", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_attn_binding(void) { return PyModule_Create(&module); }
+// torch_version: the torch whose headers this was built with (its classes' layouts are compiled in).
+PyMODINIT_FUNC PyInit_attn_binding(void) {
+    PyObject *m = PyModule_Create(&module);
+    if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", BL_TORCH_VERSION) != 0) Py_CLEAR(m);
+    return m;
+}
