@@ -172,8 +172,9 @@ bl_status bl_kv_compact(void *pool, int64_t planes, int64_t page_bytes, int32_t 
 /* float32.  cu_q, cu_k [B + 1] int32, increasing, from 0, ending at or      */
 /* before Tq, Tk (rows behind the end are left as they were); max_q, max_k:  */
 /* at least every entry's query and key count (an entry with more gives      */
-/* BL_ERR_INDEX and its further rows are not computed).  Tq, Tk, B >= 1,     */
-/* Tq * Hq and Tk * Hkv < 2^31, max_q, max_k < 2^24.                         */
+/* BL_ERR_INDEX; the gradients leave its queries from max_q on out, and      */
+/* neither o, dq from max_q on nor dk, dv from max_k on are written).        */
+/* Tq, Tk, B >= 1, Tq * Hq and Tk * Hkv < 2^31, max_q, max_k < 2^24.         */
 /* ------------------------------------------------------------------------ */
 bl_status bl_attn_forward(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                           int64_t v_stride, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,

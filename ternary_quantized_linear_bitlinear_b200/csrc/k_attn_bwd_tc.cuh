@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     const int kvh = blockIdx.y, b = blockIdx.z;
     Entry e;
     if (!entry_of(p, b, e)) return;
+    if (e.nk > p.max_k) e.nk = p.max_k;  // further keys' gradients are left as they were
     // the sink tiles' pieces come first, then the key tiles
     const int extra = cutting.sink_tiles * cutting.pieces;
     const bool far = (int)blockIdx.x < extra;
@@ -789,6 +790,7 @@ __global__ void __launch_bounds__(256) k_attn_sink_sum(const __grid_constant__ R
     const int t = blockIdx.x / AB_SUM_CTAS, kvh = blockIdx.y, b = blockIdx.z;
     Entry e;
     if (!entry_of(p, b, e)) return;
+    if (e.nk > p.max_k) e.nk = p.max_k;
     const int j0 = t * 128;
     if (j0 >= e.nk) return;
     const int keys = e.nk - j0 < 128 ? e.nk - j0 : 128;

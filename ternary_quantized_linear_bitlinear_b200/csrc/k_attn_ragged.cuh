@@ -21,7 +21,8 @@ struct RaggedParams {
 };
 
 // One batch entry: query rows q0 .. q0 + nq - 1, key rows k0 .. k0 + nk - 1;
-// query i stands at position i + off.
+// query i stands at position i + off.  Queries beyond max_q are left out (no
+// CTA computes their lse and delta, so none may read them).
 struct Entry {
     int q0, nq, k0, nk, off;
 };
@@ -34,13 +35,14 @@ __device__ __forceinline__ bool entry_of(const RaggedParams &p, int b, Entry &e)
     e.nq = q1 - q0;
     e.nk = k1 - k0;
     e.off = e.nk - e.nq;
+    if (e.nq > p.max_q) e.nq = p.max_q;
     return true;
 }
 
 // Reports an entry that a launch cannot compute as described.
 __device__ __forceinline__ void check_entry(const RaggedParams &p, int b) {
     Entry e;
-    if (!entry_of(p, b, e) || e.nq > p.max_q || e.nk > p.max_k) raise_device_error(DEVERR_INDEX);
+    if (!entry_of(p, b, e) || e.nk - e.off > p.max_q || e.nk > p.max_k) raise_device_error(DEVERR_INDEX);
 }
 
 __device__ __forceinline__ bool sees(const RaggedParams &p, int pos, int key) {
