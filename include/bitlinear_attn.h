@@ -175,6 +175,8 @@ bl_status bl_kv_compact(void *pool, int64_t planes, int64_t page_bytes, int32_t 
 /* BL_ERR_INDEX; the gradients leave its queries from max_q on out, and      */
 /* neither o, dq from max_q on nor dk, dv from max_k on are written).        */
 /* Tq, Tk, B >= 1, Tq * Hq and Tk * Hkv < 2^31, max_q, max_k < 2^24.         */
+/* The gradients' workspace is Tq * Hq floats, and with a window and sinks   */
+/* at most 4 * Tq * Hkv * D more.                                            */
 /* ------------------------------------------------------------------------ */
 bl_status bl_attn_forward(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                           int64_t v_stride, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,

@@ -511,7 +511,7 @@ size_t bl_attn_backward_workspace_bytes(int64_t Tq, int64_t Tk, int64_t Hq, int6
         return 0;
     if (max_q >= (1 << 24) || max_k >= (1 << 24) || B > 65535) return 0;
     const DkvCut cut = dkv_cut(max_q, max_k, norm_window(window), norm_sinks(sinks));
-    return align256((size_t)Tq * Hq * 4) + sink_slot(cut, (int)Hkv, (int)D, (int)B, 0, 0, 0) * 4;
+    return align256((size_t)Tq * Hq * 4) + sink_sums(cut, (int)Hkv, (int)D, sink_places(cut, Tq), 0) * 4;
 }
 
 bl_status bl_attn_backward(const void *do_, const void *q, const void *k, const void *v, const void *o,

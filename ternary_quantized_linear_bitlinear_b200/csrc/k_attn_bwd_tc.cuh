@@ -29,9 +29,10 @@
 // tile is ever transposed through shared memory.  The tensor core works one
 // step behind the threads: dV(j), S(j + 1) while they form dS(j), dK(j),
 // dP(j + 1) while they form P(j + 1).
-// A tile with sinks is seen by every later query of its sequence.  Its rows
-// beyond the window's reach are cut into pieces of their own, whose float32
-// sums go to the workspace and are added in order by k_attn_sink_sum.
+// A tile with sinks is seen by every later query of its sequence.  The query
+// tiles beyond the window's reach are cut into pieces of their own; the float32
+// sums of the sinks' rows go to the workspace and are added in order by
+// k_attn_sink_sum.
 //
 // Bound: eight products of 512 tensor cycles per pair of 128-tiles at D = 128
 // against 2 x 1024 cycles of exponentials.
@@ -416,29 +417,50 @@ static_assert(DkvShape<128>::SMEM <= 227 * 1024, "dK, dV shared memory");
 
 // How a launch is cut: `tiles` key tiles of every entry, the first
 // `sink_tiles` of them with `pieces` more CTAs each for the queries beyond the
-// window's reach, `chunk` query tiles (of every head) per piece.
+// window's reach, `chunk` query tiles (of every head) per piece; `rows` keys
+// are sinks.  An entry with at most `chunk` query tiles for a sink tile has no
+// pieces for it.
+//
+// chunk: at least as many query tiles as an ordinary key tile has, and one
+// more, so that the first piece holds all that the keys behind the sinks in the
+// last sink tile are seen by; and not fewer than the sink tiles, which bounds
+// the workspace (below).  When the sinks fill more than half of the key tiles
+// nothing is cut: those tiles are then CTAs enough.
 struct DkvCut {
-    int tiles, sink_tiles, pieces, chunk;
+    int tiles, sink_tiles, pieces, chunk, rows;
 };
 
 inline DkvCut dkv_cut(int64_t max_q, int64_t max_k, int64_t window, int64_t sinks) {
-    DkvCut c{(int)((max_k + 127) / 128), 0, 0, 0};
+    DkvCut c{(int)((max_k + 127) / 128), 0, 0, 1, 0};
     if (window > 0 && sinks > 0) {
-        const int64_t qt = (max_q + 127) / 128 + 1;
-        // as many query tiles as an ordinary key tile has
-        c.chunk = (int)((window + 127) / 128 + 1 < 4 ? 4 : (window + 127) / 128 + 1);
-        if (qt > c.chunk) {
-            const int64_t st = ((sinks < max_k ? sinks : max_k) + 127) / 128;
+        const int64_t qt = (max_q + 127) / 128, rows = sinks < max_k ? sinks : max_k, st = (rows + 127) / 128;
+        int64_t chunk = (window + 127) / 128 + 2;
+        if (chunk < 4) chunk = 4;
+        if (chunk < st) chunk = st;
+        if (qt > chunk && 2 * st <= c.tiles) {
             c.sink_tiles = (int)st;
-            c.pieces = (int)((qt + c.chunk - 1) / c.chunk);
+            c.chunk = (int)chunk;
+            c.pieces = (int)((qt + chunk - 1) / chunk - 1);
+            c.rows = (int)rows;
         }
     }
     return c;
 }
 
-// float32 sums of sink tile t of (b, kvh): [piece 0 .. pieces][dk, dv][128][D]
-__host__ __device__ inline size_t sink_slot(const DkvCut &c, int Hkv, int D, int b, int kvh, int t, int piece) {
-    return (((((size_t)b * Hkv + kvh) * c.sink_tiles + t) * (c.pieces + 1) + piece) * 2) * 128 * D;
+// float32 sums of a piece (0: the first) of an entry whose queries begin at row
+// q0, for one kv head: [dk, dv][rows][D].  An entry with k > 1 pieces has more
+// than 128 chunk (k - 1) queries, so from one entry to the next q0 / (64 chunk)
+// grows by at least 2 (k - 1) >= k: the places of different entries are apart,
+// and Tq / (64 chunk) of them are enough.  rows <= 128 chunk: at most 2 Tq rows
+// for each kv head.
+__host__ __device__ inline size_t sink_places(const DkvCut &c, int64_t Tq) {
+    return c.rows > 0 ? (size_t)(Tq / (64 * (int64_t)c.chunk)) : 0;
+}
+__host__ __device__ inline size_t sink_sums(const DkvCut &c, int Hkv, int D, size_t place, int kvh) {
+    return (place * Hkv + kvh) * 2 * c.rows * D;
+}
+__device__ __forceinline__ size_t piece_sums(const DkvCut &c, const RaggedParams &p, const Entry &e, int kvh, int piece) {
+    return sink_sums(c, p.Hkv, p.D, (size_t)(e.q0 / (64ll * c.chunk) + piece), kvh);
 }
 
 template <int DP>
@@ -481,7 +503,8 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
     if (q_lo < 0) q_lo = 0;
     int t_lo = q_lo / 128, t_hi = q_hi >= q_lo ? q_hi / 128 : t_lo - 1;  // tiles t_lo .. t_hi
     const bool sink = j0 < p.sinks && p.window > 0;
-    if (sink && t < cutting.sink_tiles) {
+    const bool to_sums = t < cutting.sink_tiles && t_hi - t_lo + 1 > cutting.chunk;
+    if (t < cutting.sink_tiles) {
         // the main CTA keeps the first `chunk` tiles, piece i the i-th `chunk` after them
         t_lo += piece * cutting.chunk;
         if (t_hi > t_lo + cutting.chunk - 1) t_hi = t_lo + cutting.chunk - 1;
@@ -489,7 +512,6 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
         const long long last = (long long)j0 + keys - 1 + p.window - 1 - e.off;
         if (last < q_hi) t_hi = last < q_lo ? t_lo - 1 : (int)(last / 128);
     }
-    const bool to_sums = t < cutting.sink_tiles;
     const int qt = t_hi - t_lo + 1 > 0 ? t_hi - t_lo + 1 : 0, n = qt * p.group;
     if (far && n == 0) return;  // (its sums are not read)
     // the walk: query tiles t_lo .. t_hi of the group's first head, then of the next
@@ -742,27 +764,23 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             // the first four warps write dV, the others dK
             const float f = c == 0 ? 1.f : p.scale;
             const u32 col = (c == 0 ? dv_col : dk_col) + lane_at;
-            if (!to_sums) {
-                // (the query stages are not read any more)
+            if (!far) {
+                // (the query stages are not read any more; what has further pieces is written again by k_attn_sink_sum)
                 const int at = 32 * (warp & 3);
                 tc_store_rows<DP>(col, n == 0, f, sm + F::OFF_Q + (warp - 4) * 32 * DP * 2,
                                   (c == 0 ? p.dv : p.dk) + ((size_t)(e.k0 + j0 + at) * p.Hkv + kvh) * p.D,
                                   (long long)p.Hkv * p.D, keys - at, p.D);
-            } else {
-                float *acc = sums + sink_slot(cutting, p.Hkv, p.D, b, kvh, t, piece) + ((size_t)(c == 0 ? 1 : 0) * 128 + r) * p.D;
+            }
+            if (to_sums && j0 + 32 * (warp & 3) < cutting.rows) {
+                float *acc = sums + piece_sums(cutting, p, e, kvh, piece) + ((size_t)(c == 0 ? cutting.rows : 0) + key) * p.D;
 #pragma unroll 1
                 for (int k = 0; k < DP / 32; ++k) {
                     u32 o[32];
-                    if (n > 0) {
-                        tc_ld32(o, col + 32 * k);
-                        tc_wait_ld();
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0u;
-                    }
+                    tc_ld32(o, col + 32 * k);
+                    tc_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
-                        if (r >= keys || 32 * k + j >= p.D) continue;
+                        if (r >= keys || key >= cutting.rows || 32 * k + j >= p.D) continue;
                         float x[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[j + i]) * f;
@@ -793,16 +811,14 @@ __global__ void __launch_bounds__(256) k_attn_sink_sum(const __grid_constant__ R
     if (e.nk > p.max_k) e.nk = p.max_k;
     const int j0 = t * 128;
     if (j0 >= e.nk) return;
-    const int keys = e.nk - j0 < 128 ? e.nk - j0 : 128;
+    const int end = e.nk < cutting.rows ? e.nk : cutting.rows, keys = end - j0 < 128 ? end - j0 : 128;
     const int q_lo = j0 - e.off > 0 ? j0 - e.off : 0;
     const int t_lo = q_lo / 128, t_hi = e.nq - 1 >= q_lo ? (e.nq - 1) / 128 : t_lo - 1;
-    // pieces that had query tiles (piece 0, the main CTA, always wrote)
     const int tiles = t_hi - t_lo + 1;
-    int pieces = (tiles + cutting.chunk - 1) / cutting.chunk;
-    if (pieces > cutting.pieces + 1) pieces = cutting.pieces + 1;
-    if (pieces < 1) pieces = 1;
-    const float *base = sums + sink_slot(cutting, p.Hkv, p.D, b, kvh, t, 0);
-    const size_t step = (size_t)2 * 128 * p.D;
+    if (tiles <= cutting.chunk) return;  // (the first piece was all)
+    const int pieces = (tiles + cutting.chunk - 1) / cutting.chunk;
+    const float *base = sums + piece_sums(cutting, p, e, kvh, 0);
+    const size_t step = sink_sums(cutting, p.Hkv, p.D, 1, 0);
     for (int i = (blockIdx.x % AB_SUM_CTAS * 256 + threadIdx.x) * 8; i < 2 * keys * p.D; i += AB_SUM_CTAS * 256 * 8) {
         const int which = i / (keys * p.D), at = i - which * keys * p.D;  // 0: dk, 1: dv
         const int r = at / p.D, d = at - r * p.D;
@@ -810,7 +826,7 @@ __global__ void __launch_bounds__(256) k_attn_sink_sum(const __grid_constant__ R
 #pragma unroll 4
         for (int k = 0; k < pieces; ++k) {
             float y[8];
-            load8<false>(reinterpret_cast<const uint8_t *>(base + k * step + ((size_t)which * 128 + r) * p.D + d), y);
+            load8<false>(reinterpret_cast<const uint8_t *>(base + k * step + ((size_t)which * cutting.rows + j0 + r) * p.D + d), y);
 #pragma unroll
             for (int c = 0; c < 8; ++c) x[c] += y[c];
         }
