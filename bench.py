@@ -1084,7 +1084,7 @@ def bench_layer3b(args, world, local, dev, pk):
         "weight_replicas": R, "launch": "one fused grouped launch over the 7 projections, its own replica each",
         "roofline": roofline_hbm("k_decode (fused act quant + GEMV, 7 problems)", wbytes + xbytes, us, pk),
         "dependent_4_launches_us_per_layer": round(us_dep, 3),
-        "dependent_note": "qkv | o | gate,up | down as four ordered launches (the attention itself is out of scope)",
+        "dependent_note": "qkv | o | gate,up | down as four ordered launches (projections alone, no attention between them)",
         "clocks": clk.summary()}
     out["value"] = out["decode_m1"]["gbs"]
     out["unit"] = "GB/s (decode M = 1)"

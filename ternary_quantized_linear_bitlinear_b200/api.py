@@ -627,7 +627,6 @@ def bl_linear_grouped(Ws, X, subln_gain=None, subln_eps: float = 1e-6, Ys=None, 
 # through the checks here.
 
 _Tensor = torch.Tensor
-_B16 = torch.bfloat16
 _I32 = torch.int32
 
 

@@ -45,10 +45,6 @@ __device__ __forceinline__ void check_entry(const RaggedParams &p, int b) {
     if (!entry_of(p, b, e) || e.nk - e.off > p.max_q || e.nk > p.max_k) raise_device_error(DEVERR_INDEX);
 }
 
-__device__ __forceinline__ bool sees(const RaggedParams &p, int pos, int key) {
-    return key <= pos && (p.window == 0 || pos - key < p.window || key < p.sinks);
-}
-
 // Key tiles of BK keys that queries at positions p0 .. p1 can see: sink tiles
 // 0 .. ns - 1, then wt .. wt + nw - 1.
 struct KeyTiles {
@@ -95,31 +91,12 @@ __device__ __forceinline__ u32 tile_at(u32 base, int row, int chunk) {
     return base + (u32)(row * DP * 2) + (u32)((chunk ^ (row & 7)) << 4);
 }
 
-// rows of a strided [T, H, D] tensor into a tile: rows beyond `rows` and
-// columns beyond D are zero.
-template <int DP, int ROWS, int T>
-__device__ __forceinline__ void load_tile(u32 base, const uint16_t *src, long long stride, int rows, int D) {
-    constexpr int C = DP / 8;
-    for (int i = threadIdx.x; i < ROWS * C; i += T) {
-        const int r = i / C, c = i - r * C;
-        const u32 dst = tile_at<DP>(base, r, c);
-        const bool ok = r < rows && c * 8 < D;
-        const uint16_t *s = ok ? src + r * stride + c * 8 : src;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(s), "r"(ok ? 16 : 0) : "memory");
-    }
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A operand (16 rows x 16 columns) of row tile `row0`, columns 16 kk ..
-template <int DP>
-__device__ __forceinline__ void a_frag(u32 (&r)[4], u32 base, int row0, int kk) {
-    const int lane = threadIdx.x & 31;
-    ldsm4(r, tile_at<DP>(base, row0 + (lane & 15), kk * 2 + (lane >> 4)));
-}
 // B operand for two n-tiles of 8 rows (n = tile rows, k = columns): r[0..1] the first, r[2..3] the second
 template <int DP>
 __device__ __forceinline__ void b_frag(u32 (&r)[4], u32 base, int row0, int kk) {
