@@ -216,6 +216,9 @@ bl_status decode_by_type(DecodeAttnParams &P, const AttnDevice &d, bool bf16_cac
         return P.gsize <= 4 ? launch_decode<DecodeMma<DP, DEC_F32_4, 4, 3, 4>>(P, d, batches, st)
                             : launch_decode<DecodeMma<DP, DEC_F32_8, 4, 3, 3>>(P, d, batches, st);
     }
+    // float32 cache: a head group's registers decide how many warps an SM holds (16 up to 3 heads, 8 above).  64 x 1028
+    // keys of 20 unshared heads of 128: 236 us for one head, 244 us in the kernel for 3, 324 us in that for 8;
+    // 64 x 3000 of 12 / 4 heads 150 us (5.2 TB/s) against 199 us.  8 heads: 3.9 TB/s, bound by the products.
     if (P.gsize == 1) return launch_decode<DecodeFma<DP, 1, 8, 2, 3>>(P, d, batches, st);
     if (P.gsize <= 3) return launch_decode<DecodeFma<DP, 3, 8, 2, 3>>(P, d, batches, st);
     return launch_decode<DecodeFma<DP, 8, 8, 1, 4>>(P, d, batches, st);

@@ -378,9 +378,11 @@ struct DecodeFma {
 // which add them by one exchange and both go on with the sum.  On the CUDA
 // cores a batch took 1220 instructions for three heads, 58 % of the issue
 // slots at half of the copy bandwidth; here 8 x 65000 keys of 12 / 4 heads
-// run at 6.3 TB/s, and the second products of DEC_F32_8 cost a quarter (4.75
-// instead of 5.9 TB/s on 64 x 1028 keys of 20 unshared heads), which is why up
-// to 4 heads do without.
+// run at 6.2 TB/s, and the second products of DEC_F32_8 cost a tenth (64 x 1028
+// keys of 20 unshared heads 130 instead of 119 us), which is why up to 4 heads
+// do without.  Groups of 8 heads of 128, 64 x 6000 keys: 52 us with bfloat16 q,
+// 73 us with float32 q (three terms' operands and 64 of output a thread: 208
+// bytes of them spill).
 // Rows go into the slots by 16-byte cp.async with the chunks permuted by the
 // row (tile_at), hidden rows as zeros.
 enum { DEC_BF16, DEC_F32_4, DEC_F32_8 };
