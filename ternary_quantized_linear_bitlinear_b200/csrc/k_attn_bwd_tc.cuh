@@ -55,7 +55,7 @@ constexpr unsigned long long AB_TIMEOUT_NS = 2000000000ull;
 
 template <int DP>
 struct DqShape {
-    static constexpr int KS = 3, VS = DP == 64 ? 3 : 2;  // stages of K (read twice, two steps apart) and V
+    static constexpr int KS = 3, VS = DP == 64 ? 3 : 2;  // stages of K (read for S, and again for dQ and R up to two steps later) and V
     static constexpr int TILE = DP / 64 * TC_BLOCK;
     static constexpr int OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE, OFF_D = OFF_V + VS * TILE;
     static constexpr int OFF_BAR = OFF_D + 2 * 128 * 4;
